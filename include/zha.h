@@ -300,6 +300,131 @@ int zha_tree_device(const zha_tree* tree);
  * rebuilt.  ZHA_ERR_INVALID_ARG on a null tree or negative cycles. */
 zha_status zha_tree_set_wait_limit(zha_tree* tree, long long cycles);
 
+/* ---- Paged KV cache -----------------------------------------------------------------
+ *
+ * Many sequences in one pool of pages.  Page p of K (and of V) holds page_tokens rows of every
+ * KV head:
+ *     K, V  [num_pages, kv_heads, page_tokens, head_dim]  (desc's kv_dtype; the caller's)
+ * A sequence occupies a slot 0 .. max_seqs - 1: a row of page ids and a length; token t is row
+ * t % page_tokens of the row's page t / page_tokens.  Several sequences may hold a page (forks of one
+ * prompt); a page no row names is free.  A partly filled last page belongs to one
+ * sequence only.
+ *
+ * Table, lengths and counts live in the caller's workspace on the device and the calls change
+ * them there, in stream order, so all calls but the init and the check can be captured into
+ * a CUDA graph and replayed while the sequences grow.  Results do not depend on timing:
+ * new pages are the lowest free ones, handed out in the order of the call's list and of each
+ * sequence's pages.
+ *
+ * A call's slot list is int32 on the device (n <= max_seqs entries; n == 0 is a no-op).  A call
+ * that hands out pages (append, fork, copy) does all of its work or none: when a slot is out of
+ * range or named twice as a destination, a destination of a fork or copy is not empty, or a
+ * count is out of range (ZHA_ERR_DEVICE), or when there are too few free pages or a sequence
+ * would outgrow max_seq_pages (ZHA_ERR_CAPACITY), nothing is changed and zha_pages_check
+ * reports it.  The handle's device must be current (ZHA_ERR_INVALID_ARG otherwise).  Calls that
+ * share a cache, and pools that calls write, are to be ordered by the caller; calls that only read it
+ * (gather, attention) may overlap one another.
+ * (The source pages have no counterpart: the cache of their method is dense.) */
+typedef struct {
+  int kv_heads;      /* >= 1                                                          */
+  int head_dim;      /* 64 or 128                                                     */
+  int page_tokens;   /* a power of two, 8 .. 256                                      */
+  int num_pages;     /* >= 1; num_pages * kv_heads <= 2^30                            */
+  int max_seqs;      /* slots, 1 .. 65535; max_seqs * max_seq_pages <= 2^30           */
+  int max_seq_pages; /* pages a sequence may hold, >= 1; page_tokens times it <= 2^30 */
+  zha_dtype kv_dtype;
+} zha_pages_desc;
+
+typedef struct zha_pages zha_pages; /* opaque host handle */
+
+/* Device bytes the caller must provide to zha_pages_init; 0 on a bad desc. */
+size_t zha_pages_workspace_bytes(const zha_pages_desc* desc);
+
+/* Creates a host handle over caller-owned workspace (256-byte aligned) and empties the cache, on
+ * `stream`.  *out receives the handle; free it with zha_pages_destroy. */
+zha_status zha_pages_init(const zha_pages_desc* desc, void* d_workspace, size_t workspace_bytes, void* stream,
+                          zha_pages** out);
+zha_status zha_pages_destroy(zha_pages* pages); /* the handle only; the workspace stays the caller's */
+
+/* Replaces the cache's state by a table [max_seqs, max_seq_pages] and lengths [max_seqs] (int32,
+ * device): a saved state, or the pages a caller filled by itself.  Entries behind a sequence's
+ * last page are not read.  A length or page id out of range, or a partly filled last page that
+ * another entry names too, leaves the cache empty and sets ZHA_ERR_DEVICE. */
+zha_status zha_pages_load(zha_pages* pages, const int* d_table, const int* d_lens, void* stream);
+
+/* Appends tokens to the listed sequences: d_Knew, d_Vnew [n, kv_heads, tokens, head_dim] in
+ * kv_dtype; entry i appends its first d_counts[i] (0 .. tokens; NULL: all). */
+zha_status zha_pages_append(zha_pages* pages, void* d_K, void* d_V, const int* d_seqs, int n, const void* d_Knew,
+                            const void* d_Vnew, int tokens, const int* d_counts, void* stream);
+
+/* Empty slot d_dst[i] becomes a fork of sequence d_src[i]: it holds the same full pages, and a
+ * copy of the rows of a partly filled last page.  A source may be named repeatedly. */
+zha_status zha_pages_fork(zha_pages* pages, void* d_K, void* d_V, const int* d_src, const int* d_dst, int n,
+                          void* stream);
+
+/* As a fork, with every page copied; `from` may be the same cache or another with the same kv_heads,
+ * head_dim, page_tokens, kv_dtype and device (its pools: d_Kfrom, d_Vfrom). */
+zha_status zha_pages_copy(const zha_pages* from, const void* d_Kfrom, const void* d_Vfrom, zha_pages* pages, void* d_K,
+                          void* d_V, const int* d_src, const int* d_dst, int n, void* stream);
+
+/* Empties the listed slots; pages no other sequence holds become free.  Empty slots and slots
+ * named twice are fine; a slot out of range is skipped and sets ZHA_ERR_DEVICE. */
+zha_status zha_pages_free(zha_pages* pages, const int* d_seqs, int n, void* stream);
+
+/* Moves the pages in use to the bottom of the pools: with `live` pages in use, the k-th free page
+ * below live receives the whole of the k-th used page at or above it, and the table follows.
+ * d_live (int32, device, nullable) receives live. */
+zha_status zha_pages_compact(zha_pages* pages, void* d_K, void* d_V, int* d_live, void* stream);
+
+/* Copies the listed sequences into a dense cache [n, kv_heads, capacity_tokens, head_dim] (the
+ * layout zha_tree_build reads); rows at or past a sequence's length stay as they are.  A slot
+ * out of range (ZHA_ERR_DEVICE) and a sequence longer than capacity_tokens (ZHA_ERR_CAPACITY)
+ * are skipped. */
+zha_status zha_pages_gather(const zha_pages* pages, const void* d_K, const void* d_V, const int* d_seqs, int n,
+                            void* d_Kout, void* d_Vout, long long capacity_tokens, void* stream);
+
+/* Exact softmax attention of a batch of cached sequences that share a prefix: the rows of
+ * every sequence are taken through the prefix's tokens together, so that its keys and values are
+ * read once for all of them, and the parts are joined by their softmax statistics (fp32).
+ *   d_Q            [batch, q_heads, nq, head_dim] in q_dtype; q_heads % kv_heads == 0
+ *   d_seqs         [batch] int32 slots (device; a slot may be named repeatedly)
+ *   prefix_tokens  tokens 0 .. prefix_tokens - 1 of every sequence are read from the pages of slot
+ *                  prefix_seq (a multiple of page_tokens; 0: nothing is shared).  The caller sees to it that
+ *                  all of the batch share them, as forks of prefix_seq do
+ *   causal         0: a query sees all len tokens of its sequence; 1: query i of nq is token
+ *                  len - nq + i and sees the tokens up to itself.  A query that sees no token gives zeros
+ *   scale          multiplies q . k before the softmax; finite
+ *   d_O            out [batch, q_heads, nq, head_dim] in o_dtype
+ *   d_scratch      >= zha_prefix_attn_scratch_bytes(pages, batch, q_heads, nq, prefix_tokens) bytes,
+ *                  16-byte aligned; contents need no initialisation.  Calls that may overlap need one each
+ * Rows of the pools that hold no token are never used, whatever they contain.  A slot out of range
+ * counts as an empty sequence, a page id out of range as a page of zeros; those, and a prefix longer than
+ * prefix_seq, set ZHA_ERR_DEVICE.  Values of tokens that any query of a call sees must be finite.
+ * bf16 queries over a bf16 cache run on the tensor cores: products are exact, sums fp32; for a bf16 output
+ * the softmax weights are rounded to bf16 before they meet V, for an fp32 output they keep 16 bits.
+ * All other types run in fp32. */
+size_t zha_prefix_attn_scratch_bytes(const zha_pages* pages, int batch, int q_heads, int nq, long long prefix_tokens);
+zha_status zha_prefix_attn_decode(const zha_pages* pages, const void* d_Q, zha_dtype q_dtype, int batch, int q_heads,
+                                  int nq, const void* d_K, const void* d_V, const int* d_seqs, int prefix_seq,
+                                  long long prefix_tokens, int causal, float scale, void* d_O, zha_dtype o_dtype,
+                                  void* d_scratch, size_t scratch_bytes, void* stream);
+
+/* Synchronizes `stream`, then reads and clears the cache's device error word: ZHA_OK,
+ * ZHA_ERR_TIMEOUT, ZHA_ERR_DEVICE or ZHA_ERR_CAPACITY (the first that applies), or ZHA_ERR_CUDA. */
+zha_status zha_pages_check(zha_pages* pages, void* stream);
+
+/* Getters.  The arrays are device memory inside the workspace: table [max_seqs, max_seq_pages] (-1
+ * behind a sequence's last page), lens [max_seqs], refs [num_pages] (sequences that hold a page). */
+const int* zha_pages_table(const zha_pages* pages);
+const int* zha_pages_lens(const zha_pages* pages);
+const int* zha_pages_refs(const zha_pages* pages);
+long long zha_pages_launch_count(const zha_pages* pages);
+zha_status zha_pages_get_desc(const zha_pages* pages, zha_pages_desc* out);
+int zha_pages_device(const zha_pages* pages);
+/* As zha_tree_set_wait_limit: bounds the attention's first wait for its copies (0: default).  Outputs
+ * of a call whose wait ran out are NaN. */
+zha_status zha_pages_set_wait_limit(zha_pages* pages, long long cycles);
+
 const char* zha_status_string(zha_status status);
 
 #ifdef __cplusplus

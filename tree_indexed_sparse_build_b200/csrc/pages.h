@@ -1,0 +1,52 @@
+// Host-side state of a paged cache and the view of its workspace that kernels take.
+#pragma once
+
+#include "zha_internal.h"
+
+namespace zha {
+
+constexpr int kNoClaim = 0x7fffffff;
+
+// The workspace of a paged cache (device pointers into the caller's buffer).
+struct PagesView {
+  unsigned* err;   // device error word
+  int* ok;         // 1: the last planned call's arguments held, its row kernel may run
+  int* free_pages; // pages that no sequence holds
+  int* moves;      // pages that a compaction moves
+  int* live;       // pages in use
+  int* lens;       // [max_seqs] tokens
+  int* claim;      // [max_seqs] lowest list entry that names a slot (kNoClaim between calls)
+  int* plan_len;   // [max_seqs] per list entry: tokens before the call (append) or of the source
+  int* plan_cnt;   // [max_seqs] tokens the entry adds
+  int* plan_base;  // [max_seqs] its first page's place in `fresh`
+  int* refs;       // [num_pages] sequences that hold a page
+  int* fresh;      // [num_pages] pages given out by the call / pages that a compaction moves
+  int* name;       // [num_pages] a moved page's new id / load's reference counts
+  unsigned* used;  // [words] bit p: page p is held (bits past num_pages are set)
+  int* table;      // [max_seqs, width] page ids, -1 behind a sequence's last page
+  int max_seqs, width, num_pages, words;
+  int page, shift;  // tokens per page, a power of two
+  int heads;        // KV heads
+  int row_vecs;     // 16-byte vectors per row (head_dim elements)
+};
+
+}  // namespace zha
+
+struct zha_pages {
+  zha_pages_desc desc;
+  zha::PagesView v;
+  int sms;
+  int device;
+  long long launches;
+  long long wait_limit;
+};
+
+namespace zha {
+
+// True when the pages' device is the current one (launches go to the current device).
+inline bool on_device(const zha_pages* p) {
+  int d = -1;
+  return cudaGetDevice(&d) == cudaSuccess && d == p->device;
+}
+
+}  // namespace zha

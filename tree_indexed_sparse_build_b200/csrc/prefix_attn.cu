@@ -1,0 +1,496 @@
+// Attention over a shared prefix and each sequence's own pages: the plan, the fp32 kernel and the
+// join of the partial results.  (bf16 queries over a bf16 cache: prefix_attn_tc.cu.)
+#include <cmath>
+#include <cstdint>
+
+#include "prefix_attn.cuh"
+
+using namespace zha;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kKeys = 64;  // keys per tile of the fp32 kernel
+
+// ---------------------------------------------------------------- fp32 kernel
+//
+// A tile of RT rows against 64 keys at a time, everything in fp32 on the FMA pipes: thread
+// (ty, tx) forms the scores of rows ty * RT/16 .. and keys tx, tx + 16, .., keeps those rows'
+// running maximum and sum (the 16 threads of a row agree on them by shuffles) and
+// accumulates columns 4 tx .. of the same rows.  K and V take turns in one buffer, so that two
+// CTAs share an SM and one's loads cover the other's arithmetic.
+template <int D, typename TQ, typename TKV>
+struct Fp32Tile {
+  static constexpr int kStride = D + 4;  // 16 rows apart by 4 banks: float4 reads without conflicts
+  static constexpr int kPStride = kKeys + 4;
+
+  // Keys [t0, t0 + n) of the sequence whose page ids are `row` to smem; rows past n are zeros.
+  __device__ static void load_keys(const PagesView& v, const TKV* pool, const int* row, int head, int t0, int n,
+                                   float* sm) {
+    constexpr int vec = 16 / sizeof(TKV), per = D / vec;
+    for (int i = threadIdx.x; i < kKeys * per; i += kThreads) {
+      const int r = i / per, c = i % per;
+      float f[vec];
+      if (r < n) {
+        const int t = t0 + r, page = row[t >> v.shift];
+        if ((unsigned)page < (unsigned)v.num_pages) {
+          const TKV* src = pool + (((size_t)page * v.heads + head) * v.page + (t & (v.page - 1))) * D + c * vec;
+          Vec16<TKV>::to_f32(*reinterpret_cast<const uint4*>(src), f);
+        } else {
+          atomicOr(v.err, kDevErrBadSeq);
+#pragma unroll
+          for (int k = 0; k < vec; ++k) f[k] = 0.f;
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < vec; ++k) f[k] = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < vec; k += 4)
+        *reinterpret_cast<float4*>(&sm[r * kStride + c * vec + k]) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+    }
+  }
+
+  template <int RT>
+  __device__ static void segment(const PrefixArgs& a, const Segment& g, float* smem) {
+    constexpr int R = RT / 16, C = D / 64;
+    const PrefixShape& s = a.s;
+    float* qs = smem;
+    float* kv = qs + 64 * kStride;
+    float* ps = kv + kKeys * kStride;
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+
+    // row r of the tile -> (sequence, row within it)
+    auto place = [&](int r, int* b, int* rem) {
+      if (g.own) {
+        *b = g.b;
+        *rem = g.tile * s.own_tile + r;
+        return *rem < s.rows && r < s.own_tile;
+      }
+      if (s.seqs_per_tile) {
+        *b = g.tile * s.seqs_per_tile + r / s.rows;
+        *rem = r % s.rows;
+        return r < s.seqs_per_tile * s.rows && *b < s.batch;
+      }
+      *b = g.tile / s.tiles_per_seq;
+      *rem = (g.tile % s.tiles_per_seq) * s.prefix_tile + r;
+      return *rem < s.rows;
+    };
+
+    __syncthreads();  // the last segment is done with shared memory
+    constexpr int qvec = 16 / sizeof(TQ), qper = D / qvec;
+    for (int i = tid; i < RT * qper; i += kThreads) {
+      const int r = i / qper, c = i % qper;
+      int b, rem;
+      float f[qvec];
+      if (place(r, &b, &rem)) {
+        const TQ* src = static_cast<const TQ*>(a.Q) + (((size_t)b * s.heads + g.head) * s.rows + rem) * D + c * qvec;
+        Vec16<TQ>::to_f32(*reinterpret_cast<const uint4*>(src), f);
+      } else {
+#pragma unroll
+        for (int k = 0; k < qvec; ++k) f[k] = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < qvec; ++k) qs[r * kStride + c * qvec + k] = f[k];
+    }
+
+    // what each of this thread's rows sees
+    bool valid[R];
+    int seen[R];
+    float m[R], l[R], acc[R][4 * C];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      int b = 0, rem = 0, slot;
+      valid[i] = place(ty * R + i, &b, &rem);
+      seen[i] = valid[i] ? tokens_seen(s, prefix_len(a, b, &slot), rem % s.nq) : 0;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4 * C; ++c) acc[i][c] = 0.f;
+    }
+    int slot = s.prefix_seq, first = 0, end = s.prefix;
+    if (g.own) {
+      end = prefix_len(a, g.b, &slot);
+      first = s.prefix;
+    }
+    const int* pages = a.v.table + (size_t)slot * a.v.width;
+    const TKV* K = static_cast<const TKV*>(a.K);
+    const TKV* V = static_cast<const TKV*>(a.V);
+
+    for (int t = g.t0; t < g.t1; ++t) {
+      const int k0 = first + t * kKeys, n = min(kKeys, end - k0);
+      __syncthreads();
+      load_keys(a.v, K, pages, g.head, k0, n, kv);
+      __syncthreads();
+      float sc[R][4];
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc[i][j] = 0.f;
+#pragma unroll 4
+      for (int c = 0; c < D; c += 4) {
+        float4 q[R], k[4];
+#pragma unroll
+        for (int i = 0; i < R; ++i) q[i] = *reinterpret_cast<const float4*>(&qs[(ty * R + i) * kStride + c]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const float4*>(&kv[(tx + 16 * j) * kStride + c]);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            sc[i][j] = fmaf(q[i].x, k[j].x, sc[i][j]);
+            sc[i][j] = fmaf(q[i].y, k[j].y, sc[i][j]);
+            sc[i][j] = fmaf(q[i].z, k[j].z, sc[i][j]);
+            sc[i][j] = fmaf(q[i].w, k[j].w, sc[i][j]);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        float top = m[i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int key = tx + 16 * j;
+          sc[i][j] = key < n && k0 + key < seen[i] ? sc[i][j] * a.scale_log2 : -INFINITY;
+          top = fmaxf(top, sc[i][j]);
+        }
+#pragma unroll
+        for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float base = top == -INFINITY ? 0.f : top;  // a row that has seen nothing yet
+        const float fix = exp2f(m[i] - base);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float p = exp2f(sc[i][j] - base);
+          ps[(ty * R + i) * kPStride + tx + 16 * j] = p;
+          sum += p;
+        }
+#pragma unroll
+        for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        l[i] = l[i] * fix + sum;
+        m[i] = top;
+#pragma unroll
+        for (int c = 0; c < 4 * C; ++c) acc[i][c] *= fix;
+      }
+      __syncthreads();
+      load_keys(a.v, V, pages, g.head, k0, n, kv);
+      __syncthreads();
+#pragma unroll 4
+      for (int key = 0; key < kKeys; ++key) {
+        float p[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) p[i] = ps[(ty * R + i) * kPStride + key];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const float4 x = *reinterpret_cast<const float4*>(&kv[key * kStride + 64 * c + 4 * tx]);
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            acc[i][4 * c + 0] = fmaf(p[i], x.x, acc[i][4 * c + 0]);
+            acc[i][4 * c + 1] = fmaf(p[i], x.y, acc[i][4 * c + 1]);
+            acc[i][4 * c + 2] = fmaf(p[i], x.z, acc[i][4 * c + 2]);
+            acc[i][4 * c + 3] = fmaf(p[i], x.w, acc[i][4 * c + 3]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (!valid[i]) continue;
+      const size_t r = (size_t)g.slot + ty * R + i;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        *reinterpret_cast<float4*>(a.acc + r * D + 64 * c + 4 * tx) =
+            make_float4(acc[i][4 * c], acc[i][4 * c + 1], acc[i][4 * c + 2], acc[i][4 * c + 3]);
+      if (tx == 0) a.ml[r] = make_float2(m[i], l[i]);
+    }
+  }
+
+  static constexpr size_t kSmem = ((64 + kKeys) * kStride + 64 * kPStride) * sizeof(float);
+};
+
+template <int D, typename TQ, typename TKV>
+__global__ void __launch_bounds__(kThreads, 2) fp32_kernel(const __grid_constant__ PrefixArgs a) {
+  extern __shared__ float smem[];
+  __shared__ long long share[kThreads / 32 + 4];
+  pdl_wait();
+  pdl_release();
+  using Tile = Fp32Tile<D, TQ, TKV>;
+  Walk w = find_share(a, blockIdx.x, kThreads, share);
+  Segment g;
+  while (w.next(a, blockIdx.x, &g)) {
+    if ((g.own ? a.s.own_tile : a.s.prefix_tile) == 16)
+      Tile::template segment<16>(a, g, smem);
+    else
+      Tile::template segment<64>(a, g, smem);
+  }
+}
+
+// ---------------------------------------------------------------- join
+//
+// One CTA per output row: its warps take the row's partial results in turn, rescale by the
+// maxima and add (fp32); the order is fixed, so the result does not depend on timing.
+constexpr int kJoinWarps = 8;
+
+struct Part {
+  float m, l;
+};
+
+template <int D>
+struct Joined {
+  float m = -INFINITY, l = 0.f, acc[D / 32];
+  __device__ __forceinline__ Joined() {
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) acc[c] = 0.f;
+  }
+  __device__ __forceinline__ void add(float pm, float pl, const float* px) {
+    const float top = fmaxf(m, pm);
+    if (top == -INFINITY) return;
+    const float x = exp2f(m - top), y = exp2f(pm - top);
+    m = top;
+    l = l * x + pl * y;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) acc[c] = acc[c] * x + px[c] * y;
+  }
+};
+
+// The CTA whose share holds cost position x.
+__device__ __forceinline__ int cta_of(long long x, long long T, int ctas) { return (int)(((x + 1) * ctas - 1) / T); }
+
+// Key tiles of an item (first at cost `start`, `n` of cost w each) in CTA c's share.
+__device__ __forceinline__ int tiles_in(long long start, int n, int w, int c, long long T, int ctas) {
+  const long long lo = c * T / ctas, hi = (c + 1) * T / ctas;
+  long long t0 = lo > start ? (lo - start + w - 1) / w : 0;
+  long long t1 = hi > start ? (hi - start + w - 1) / w : 0;
+  if (t1 > n) t1 = n;
+  return t1 > t0 ? (int)(t1 - t0) : 0;
+}
+
+template <int D, typename TO>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ PrefixArgs a) {
+  __shared__ float s_acc[kJoinWarps][D];
+  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
+  pdl_wait();
+  pdl_release();
+  const PrefixShape& s = a.s;
+  const long long at = blockIdx.x;  // (sequence, head, row)
+  const int rem = (int)(at % s.rows), head = (int)(at / s.rows % s.heads), b = (int)(at / s.rows / s.heads);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int group = s.heads * s.own_tiles;
+  const long long T = s.prefix_cost + a.cum[s.batch] * group;
+  Joined<D> sum;
+  auto take = [&](long long row) {
+    const float2 x = a.ml[row];
+    float y[D / 32];
+    if (D == 128) {
+      const float4 z = *reinterpret_cast<const float4*>(a.acc + row * D + 4 * lane);
+      y[0] = z.x, y[1] = z.y, y[D / 32 - 2] = z.z, y[D / 32 - 1] = z.w;
+    } else {
+      const float2 z = *reinterpret_cast<const float2*>(a.acc + row * D + 2 * lane);
+      y[0] = z.x, y[1] = z.y;
+    }
+    sum.add(x.x, x.y, y);
+  };
+  if (s.prefix > 0) {
+    int rt, r;
+    if (s.seqs_per_tile) {
+      rt = b / s.seqs_per_tile;
+      r = b % s.seqs_per_tile * s.rows + rem;
+    } else {
+      rt = b * s.tiles_per_seq + rem / s.prefix_tile;
+      r = rem % s.prefix_tile;
+    }
+    const int pair = rt < 2 * s.duals ? rt >> 1 : rt - s.duals;
+    const bool dual = pair < s.duals;
+    const int w = dual ? s.dual_cost : 1;
+    const long long one = (long long)s.prefix_keys * s.dual_cost;
+    const long long start = head * s.head_cost + (dual ? pair * one : s.duals * one + (long long)(pair - s.duals) * s.prefix_keys);
+    const long long slot = (long long)head * s.pairs + pair;
+    const int c0 = cta_of(start, T, s.ctas), c1 = cta_of(start + (long long)(s.prefix_keys - 1) * w, T, s.ctas);
+    const int streams = dual ? 1 : s.streams;
+    for (int i = warp; i < (c1 - c0 + 1) * streams; i += kJoinWarps) {
+      const int c = c0 + i / streams, st = i % streams;
+      if (tiles_in(start, s.prefix_keys, w, c, T, s.ctas) <= st) continue;
+      take((slot + c) * s.prefix_slot_rows + (dual ? (rt & 1) * s.prefix_tile : st * s.prefix_tile) + r);
+    }
+  }
+  const int n = (int)(a.cum[b + 1] - a.cum[b]);
+  if (n > 0) {
+    const int item = head * s.own_tiles + rem / s.own_tile, r = rem % s.own_tile;
+    const long long start = s.prefix_cost + a.cum[b] * group + (long long)item * n;
+    const int c0 = cta_of(start, T, s.ctas), c1 = cta_of(start + n - 1, T, s.ctas);
+    for (int i = warp; i < (c1 - c0 + 1) * s.streams; i += kJoinWarps) {
+      const int c = c0 + i / s.streams, st = i % s.streams;
+      if (tiles_in(start, n, 1, c, T, s.ctas) <= st) continue;
+      take(s.own_slot0 + ((long long)b * group + item + c) * s.own_slot_rows + st * (s.own_slot_rows / s.streams) + r);
+    }
+  }
+  if (lane == 0) {
+    s_m[warp] = sum.m;
+    s_l[warp] = sum.l;
+  }
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) s_acc[warp][lane * (D / 32) + c] = sum.acc[c];
+  __syncthreads();
+  if (warp != 0) return;
+  Joined<D> all;
+#pragma unroll
+  for (int i = 0; i < kJoinWarps; ++i) all.add(s_m[i], s_l[i], &s_acc[i][lane * (D / 32)]);
+  int slot;
+  const bool sees = tokens_seen(s, prefix_len(a, b, &slot), rem % s.nq) > 0;
+  const bool lost = (*a.v.err & kDevErrTimeout) != 0;
+  TO* O = static_cast<TO*>(a.O) + at * D + lane * (D / 32);
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    const float x = lost ? NAN : sees ? all.acc[c] / all.l : 0.f;
+    if constexpr (sizeof(TO) == 2)
+      O[c] = f32_to_bf16_bits(x);
+    else
+      O[c] = x;
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+template <int D, typename TQ, typename TKV>
+cudaError_t launch_fp32(const PrefixArgs& a, cudaStream_t s) {
+  auto kern = fp32_kernel<D, TQ, TKV>;
+  const size_t smem = Fp32Tile<D, TQ, TKV>::kSmem;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(a.s.ctas), dim3(kThreads), smem, s, a);
+}
+
+template <int D>
+cudaError_t launch_fp32_types(const PrefixArgs& a, zha_dtype q, zha_dtype kv, cudaStream_t s) {
+  if (q == ZHA_F32) return kv == ZHA_F32 ? launch_fp32<D, float, float>(a, s) : launch_fp32<D, float, uint16_t>(a, s);
+  return kv == ZHA_F32 ? launch_fp32<D, uint16_t, float>(a, s) : launch_fp32<D, uint16_t, uint16_t>(a, s);
+}
+
+template <int D>
+cudaError_t launch_join(const PrefixArgs& a, zha_dtype o, cudaStream_t s) {
+  const dim3 grid((unsigned)((long long)a.s.batch * a.s.heads * a.s.rows)), block(kJoinWarps * 32);
+  return o == ZHA_BF16 ? launch_pdl(join_kernel<D, uint16_t>, grid, block, 0, s, a)
+                       : launch_pdl(join_kernel<D, float>, grid, block, 0, s, a);
+}
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
+
+// The cut of a call.  Returns false on sizes outside the kernels' index ranges.
+bool plan(const zha_pages* p, int batch, int q_heads, int nq, long long prefix, bool tensor, PrefixShape* s) {
+  const int heads = p->desc.kv_heads;
+  if (batch < 1 || nq < 1 || q_heads < 1 || q_heads % heads) return false;
+  const long long rows = (long long)(q_heads / heads) * nq;
+  if (rows > 1 << 20 || (long long)batch * heads * rows > 1LL << 30 || batch > 1 << 20) return false;
+  *s = PrefixShape{};
+  s->batch = batch;
+  s->heads = heads;
+  s->rows = (int)rows;
+  s->nq = nq;
+  s->prefix = (int)prefix;
+  s->tile_keys = tensor ? 128 : kKeys;
+  // fp32: 16 rows at a time where there are no more, else 64 (the arithmetic is per tile row)
+  s->prefix_tile = tensor ? 128 : rows * batch <= 16 ? 16 : 64;
+  s->own_tile = tensor ? 128 : rows <= 16 ? 16 : 64;
+  if (rows <= s->prefix_tile) {
+    s->seqs_per_tile = s->prefix_tile / (int)rows;
+    s->row_tiles = ceil_div(batch, s->seqs_per_tile);
+  } else {
+    s->tiles_per_seq = ceil_div(rows, s->prefix_tile);
+    s->row_tiles = batch * s->tiles_per_seq;
+  }
+  s->duals = tensor ? s->row_tiles / 2 : 0;
+  s->pairs = s->row_tiles - s->duals;
+  s->streams = tensor ? 2 : 1;
+  s->own_tiles = ceil_div(rows, s->own_tile);
+  s->prefix_keys = ceil_div(prefix, s->tile_keys);
+  s->dual_cost = 2;
+  s->ctas = tensor ? p->sms : 2 * p->sms;
+  s->head_cost = ((long long)s->duals * s->dual_cost + (s->pairs - s->duals)) * s->prefix_keys;
+  s->prefix_cost = s->head_cost * heads;
+  s->prefix_slot_rows = tensor ? 2 * s->prefix_tile : s->prefix_tile;
+  s->own_slot_rows = s->streams * (int)(rows < s->own_tile ? rows : s->own_tile);
+  s->own_slot0 = prefix > 0 ? ((long long)s->pairs * heads + s->ctas) * s->prefix_slot_rows : 0;
+  return true;
+}
+
+bool tensor_path(const zha_pages* p, zha_dtype q) { return false; }
+
+struct Scratch {
+  size_t cum, ml, acc, bytes;
+};
+
+Scratch scratch_of(const zha_pages* p, const PrefixShape& s) {
+  const long long rows =
+      s.own_slot0 + ((long long)s.batch * s.heads * s.own_tiles + s.ctas) * s.own_slot_rows;
+  Scratch x;
+  x.cum = 0;
+  x.ml = ((size_t)(s.batch + 1) * 8 + 255) / 256 * 256;
+  x.acc = x.ml + ((size_t)rows * 8 + 255) / 256 * 256;
+  x.bytes = x.acc + (size_t)rows * p->desc.head_dim * 4;
+  return x;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t zha_prefix_attn_scratch_bytes(const zha_pages* p, int batch, int q_heads, int nq, long long prefix_tokens) {
+  if (!p || prefix_tokens < 0 || prefix_tokens > 1LL << 30) return 0;
+  PrefixShape s;
+  size_t most = 0;
+  for (int tensor = 0; tensor < 2; ++tensor) {  // whatever the queries' type
+    if (tensor && p->desc.kv_dtype != ZHA_BF16) break;
+    if (!plan(p, batch, q_heads, nq, prefix_tokens, tensor != 0, &s)) return 0;
+    const size_t n = scratch_of(p, s).bytes;
+    if (n > most) most = n;
+  }
+  return most;
+}
+
+zha_status zha_prefix_attn_decode(const zha_pages* p, const void* d_Q, zha_dtype q_dtype, int batch, int q_heads, int nq,
+                                  const void* d_K, const void* d_V, const int* d_seqs, int prefix_seq,
+                                  long long prefix_tokens, int causal, float scale, void* d_O, zha_dtype o_dtype,
+                                  void* d_scratch, size_t scratch_bytes, void* stream) {
+  if (!p || batch < 0 || q_heads < 1 || nq < 0) return ZHA_ERR_INVALID_ARG;
+  if ((q_dtype != ZHA_F32 && q_dtype != ZHA_BF16) || (o_dtype != ZHA_F32 && o_dtype != ZHA_BF16))
+    return ZHA_ERR_INVALID_ARG;
+  if (q_heads % p->desc.kv_heads != 0 || !std::isfinite(scale)) return ZHA_ERR_INVALID_ARG;
+  if (prefix_tokens < 0 || prefix_tokens % p->desc.page_tokens != 0) return ZHA_ERR_INVALID_ARG;
+  if (prefix_tokens > (long long)p->desc.max_seq_pages * p->desc.page_tokens) return ZHA_ERR_CAPACITY;
+  if (prefix_tokens > 0 && (prefix_seq < 0 || prefix_seq >= p->desc.max_seqs)) return ZHA_ERR_INVALID_ARG;
+  if (!on_device(p)) return ZHA_ERR_INVALID_ARG;
+  if (batch == 0 || nq == 0) return ZHA_OK;
+  if (!d_Q || !d_K || !d_V || !d_seqs || !d_O || !d_scratch) return ZHA_ERR_INVALID_ARG;
+  if (!aligned(d_Q, 16) || !aligned(d_K, 16) || !aligned(d_V, 16) || !aligned(d_O, 16) || !aligned(d_seqs, 4) ||
+      !aligned(d_scratch, 16))
+    return ZHA_ERR_INVALID_ARG;
+  PrefixArgs a;
+  const bool tensor = tensor_path(p, q_dtype);
+  if (!plan(p, batch, q_heads, nq, prefix_tokens, tensor, &a.s)) return ZHA_ERR_UNSUPPORTED;
+  if (scratch_bytes < zha_prefix_attn_scratch_bytes(p, batch, q_heads, nq, prefix_tokens)) return ZHA_ERR_INVALID_ARG;
+  const Scratch x = scratch_of(p, a.s);
+  char* base = static_cast<char*>(d_scratch);
+  a.s.causal = causal != 0;
+  a.s.prefix_seq = prefix_tokens > 0 ? prefix_seq : 0;
+  a.v = p->v;
+  a.Q = d_Q;
+  a.K = d_K;
+  a.V = d_V;
+  a.seqs = d_seqs;
+  a.cum = reinterpret_cast<long long*>(base + x.cum);
+  a.ml = reinterpret_cast<float2*>(base + x.ml);
+  a.acc = reinterpret_cast<float*>(base + x.acc);
+  a.O = d_O;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.wait_cycles = p->wait_limit > 0 ? p->wait_limit : kCopyWaitCycles;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int d = p->desc.head_dim;
+  cudaError_t e = d == 64 ? launch_fp32_types<64>(a, q_dtype, p->desc.kv_dtype, s)
+                          : launch_fp32_types<128>(a, q_dtype, p->desc.kv_dtype, s);
+  if (e == cudaSuccess) e = d == 64 ? launch_join<64>(a, o_dtype, s) : launch_join<128>(a, o_dtype, s);
+  const_cast<zha_pages*>(p)->launches += 2;  // the handle is logically const
+  return e == cudaSuccess ? ZHA_OK : ZHA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -14,7 +14,12 @@ constexpr int kMaxBeam = 1024;
 constexpr int kMaxCandidates = 4096;  // beam * branching bound for the route kernel
 
 // Bits of the device error word.
-enum : unsigned { kDevErrTimeout = 1u, kDevErrBadLeaf = 2u };
+enum : unsigned {
+  kDevErrTimeout = 1u,
+  kDevErrBadLeaf = 2u,
+  kDevErrPool = 4u,    // a paged cache: not enough free pages, or a sequence past its row or buffer
+  kDevErrBadSeq = 8u   // a paged cache: a bad slot, list, count, table or page id
+};
 
 // Bound, in SM clock cycles, on every wait for a kernel's bulk copies (about a second).  A wait
 // that runs out records kDevErrTimeout; the kernel then waits for the copies it issued with

@@ -5,10 +5,11 @@ device pointers, the current torch stream becomes the cudaStream_t.  Every step
 of the computation runs in libzha's CUDA kernels; there is no other code path,
 and importing this module fails loudly when libzha.so has not been built.
 
-``Tree`` bundles a handle with a caller-owned workspace tensor for convenience.
+``Tree`` and ``Pages`` bundle a handle with a caller-owned workspace tensor for convenience.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -30,6 +31,11 @@ EXPORTED = [
     "zha_decode", "zha_decode_step", "zha_route_causal", "zha_decode_causal",
     "zha_tree_radii_bytes", "zha_tree_attach_radii", "zha_threshold_route", "zha_decode_buffered",
     "zha_tree_get_desc", "zha_tree_device", "zha_tree_set_wait_limit",
+    "zha_pages_workspace_bytes", "zha_pages_init", "zha_pages_destroy", "zha_pages_load",
+    "zha_pages_append", "zha_pages_fork", "zha_pages_copy", "zha_pages_free", "zha_pages_compact",
+    "zha_pages_gather", "zha_pages_check", "zha_pages_table", "zha_pages_lens", "zha_pages_refs",
+    "zha_pages_launch_count", "zha_pages_get_desc", "zha_pages_device", "zha_pages_set_wait_limit",
+    "zha_prefix_attn_scratch_bytes", "zha_prefix_attn_decode",
 ]
 
 
@@ -38,6 +44,12 @@ class zha_tree_desc(ctypes.Structure):
                 ("branching", ctypes.c_int), ("leaf_block", ctypes.c_int),
                 ("capacity_tokens", ctypes.c_longlong), ("kv_dtype", ctypes.c_int),
                 ("summary_dtype", ctypes.c_int)]
+
+
+class zha_pages_desc(ctypes.Structure):
+    _fields_ = [("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("page_tokens", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("max_seqs", ctypes.c_int), ("max_seq_pages", ctypes.c_int),
+                ("kv_dtype", ctypes.c_int)]
 
 
 class ZhaError(RuntimeError):
@@ -94,6 +106,27 @@ def lib() -> ctypes.CDLL:
             "zha_tree_get_desc": (_I, [_P, ctypes.POINTER(zha_tree_desc)]),
             "zha_tree_device": (_I, [_P]),
             "zha_tree_set_wait_limit": (_I, [_P, _LL]),
+            "zha_pages_workspace_bytes": (_SZ, [ctypes.POINTER(zha_pages_desc)]),
+            "zha_pages_init": (_I, [ctypes.POINTER(zha_pages_desc), _P, _SZ, _P, ctypes.POINTER(_P)]),
+            "zha_pages_destroy": (_I, [_P]),
+            "zha_pages_load": (_I, [_P, _P, _P, _P]),
+            "zha_pages_append": (_I, [_P, _P, _P, _P, _I, _P, _P, _I, _P, _P]),
+            "zha_pages_fork": (_I, [_P, _P, _P, _P, _P, _I, _P]),
+            "zha_pages_copy": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _P]),
+            "zha_pages_free": (_I, [_P, _P, _I, _P]),
+            "zha_pages_compact": (_I, [_P, _P, _P, _P, _P]),
+            "zha_pages_gather": (_I, [_P, _P, _P, _P, _I, _P, _P, _LL, _P]),
+            "zha_pages_check": (_I, [_P, _P]),
+            "zha_pages_table": (_P, [_P]),
+            "zha_pages_lens": (_P, [_P]),
+            "zha_pages_refs": (_P, [_P]),
+            "zha_pages_launch_count": (_LL, [_P]),
+            "zha_pages_get_desc": (_I, [_P, ctypes.POINTER(zha_pages_desc)]),
+            "zha_pages_device": (_I, [_P]),
+            "zha_pages_set_wait_limit": (_I, [_P, _LL]),
+            "zha_prefix_attn_scratch_bytes": (_SZ, [_P, _I, _I, _I, _LL]),
+            "zha_prefix_attn_decode": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _P, _I, _LL, _I, ctypes.c_float,
+                                            _P, _I, _P, _SZ, _P]),
             "zha_status_string": (ctypes.c_char_p, [_I]),
         }
         for name, (res, args) in sig.items():
@@ -422,7 +455,191 @@ def zha_tree_launch_count(handle) -> int:
     return int(lib().zha_tree_launch_count(handle))
 
 
-# ---------------------------------------------------------------- convenience owner
+# ---------------------------------------------------------------- paged cache
+
+def zha_pages_workspace_bytes(desc: zha_pages_desc) -> int:
+    return int(lib().zha_pages_workspace_bytes(ctypes.byref(desc)))
+
+
+def zha_pages_init(desc: zha_pages_desc, workspace: torch.Tensor, stream=None) -> ctypes.c_void_p:
+    h = ctypes.c_void_p()
+    _check(lib().zha_pages_init(ctypes.byref(desc), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                _stream(stream), ctypes.byref(h)), "zha_pages_init")
+    return h
+
+
+def zha_pages_destroy(handle) -> None:
+    _check(lib().zha_pages_destroy(handle), "zha_pages_destroy")
+
+
+def zha_pages_get_desc(handle) -> zha_pages_desc:
+    d = zha_pages_desc()
+    _check(lib().zha_pages_get_desc(handle, ctypes.byref(d)), "zha_pages_get_desc")
+    return d
+
+
+def zha_pages_device(handle) -> int:
+    return int(lib().zha_pages_device(handle))
+
+
+def zha_pages_set_wait_limit(handle, cycles: int) -> None:
+    """Test hook: bound the attention's first wait for its copies to `cycles` SM clocks (0: default)."""
+    _check(lib().zha_pages_set_wait_limit(handle, int(cycles)), "zha_pages_set_wait_limit")
+
+
+def zha_pages_launch_count(handle) -> int:
+    return int(lib().zha_pages_launch_count(handle))
+
+
+def zha_pages_table(handle) -> int:
+    """Device address of the page table (Pages.table is a view of it); likewise lens and refs."""
+    return int(lib().zha_pages_table(handle) or 0)
+
+
+def zha_pages_lens(handle) -> int:
+    return int(lib().zha_pages_lens(handle) or 0)
+
+
+def zha_pages_refs(handle) -> int:
+    return int(lib().zha_pages_refs(handle) or 0)
+
+
+def _pools(d: zha_pages_desc, *pools, names="KV") -> None:
+    """Refuse a pool of another type or size than [num_pages, kv_heads, page_tokens, head_dim]."""
+    n = d.num_pages * d.kv_heads * d.page_tokens * d.head_dim
+    for name, t in zip(names, pools):
+        if t.dtype != _TORCH_DT[d.kv_dtype]:
+            raise ValueError(f"{name}: dtype {t.dtype}, the cache's pools are {_TORCH_DT[d.kv_dtype]}")
+        if t.numel() != n:
+            raise ValueError(f"{name}: {t.numel()} elements, the cache's [num_pages, kv_heads, page_tokens, "
+                             f"head_dim] pool has {n}")
+
+
+def _slots(seqs: torch.Tensor, what: str, n: int | None = None) -> int:
+    _expect(seqs, what, seqs.numel() if n is None else n, _I32)
+    return seqs.numel()
+
+
+def _rows(d: zha_pages_desc, n: int, K: torch.Tensor, V: torch.Tensor, what: str) -> int:
+    """K and V [n, kv_heads, tokens, head_dim] in the cache's type; returns tokens."""
+    for name, t in (("K" + what, K), ("V" + what, V)):
+        if t.dtype != _TORCH_DT[d.kv_dtype]:
+            raise ValueError(f"{name}: dtype {t.dtype}, the cache holds {_TORCH_DT[d.kv_dtype]}")
+        if t.dim() != 4 or t.shape[:2] != (n, d.kv_heads) or t.shape[3] != d.head_dim or t.shape != K.shape:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{n}, {d.kv_heads}, tokens, {d.head_dim}], "
+                             "the same for K and V")
+    return K.shape[2]
+
+
+def _here(handle, *tensors) -> None:
+    """Refuse tensors of another device than the cache's: its kernels run on that one."""
+    dev = zha_pages_device(handle)
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, the cache is on cuda:{dev}")
+
+
+def zha_pages_load(handle, table: torch.Tensor, lens: torch.Tensor, stream=None) -> None:
+    d = zha_pages_get_desc(handle)
+    _expect(table, "table", d.max_seqs * d.max_seq_pages, _I32)
+    _expect(lens, "lens", d.max_seqs, _I32)
+    _here(handle, table, lens)
+    _check(lib().zha_pages_load(handle, _ptr(table), _ptr(lens), _stream(stream)), "zha_pages_load")
+
+
+def zha_pages_append(handle, K: torch.Tensor, V: torch.Tensor, seqs: torch.Tensor, K_new: torch.Tensor,
+                     V_new: torch.Tensor, counts: torch.Tensor | None = None, stream=None) -> None:
+    """Append K_new, V_new [n, kv_heads, tokens, head_dim] to slots seqs [n]; counts [n]: tokens of
+    each entry that count (None: all)."""
+    d = zha_pages_get_desc(handle)
+    _pools(d, K, V)
+    n = _slots(seqs, "seqs")
+    T = _rows(d, n, K_new, V_new, "_new")
+    _expect(counts, "counts", n, _I32)
+    _here(handle, K, V, seqs, K_new, V_new, counts)
+    _check(lib().zha_pages_append(handle, _ptr(K), _ptr(V), _ptr(seqs), n, _ptr(K_new), _ptr(V_new), T,
+                                  _ptr(counts), _stream(stream)), "zha_pages_append")
+
+
+def zha_pages_fork(handle, K: torch.Tensor, V: torch.Tensor, src: torch.Tensor, dst: torch.Tensor,
+                   stream=None) -> None:
+    """Empty slots dst [n] become forks of sequences src [n]."""
+    _pools(zha_pages_get_desc(handle), K, V)
+    n = _slots(src, "src")
+    _slots(dst, "dst", n)
+    _here(handle, K, V, src, dst)
+    _check(lib().zha_pages_fork(handle, _ptr(K), _ptr(V), _ptr(src), _ptr(dst), n, _stream(stream)),
+           "zha_pages_fork")
+
+
+def zha_pages_copy(from_handle, K_from: torch.Tensor, V_from: torch.Tensor, handle, K: torch.Tensor,
+                   V: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
+    """Empty slots dst [n] become copies of sequences src [n] of the cache from_handle."""
+    _pools(zha_pages_get_desc(from_handle), K_from, V_from, names=("K_from", "V_from"))
+    _pools(zha_pages_get_desc(handle), K, V)
+    n = _slots(src, "src")
+    _slots(dst, "dst", n)
+    _here(handle, K_from, V_from, K, V, src, dst)
+    _check(lib().zha_pages_copy(from_handle, _ptr(K_from), _ptr(V_from), handle, _ptr(K), _ptr(V), _ptr(src),
+                                _ptr(dst), n, _stream(stream)), "zha_pages_copy")
+
+
+def zha_pages_free(handle, seqs: torch.Tensor, stream=None) -> None:
+    n = _slots(seqs, "seqs")
+    _here(handle, seqs)
+    _check(lib().zha_pages_free(handle, _ptr(seqs), n, _stream(stream)), "zha_pages_free")
+
+
+def zha_pages_compact(handle, K: torch.Tensor, V: torch.Tensor, live: torch.Tensor | None = None,
+                      stream=None) -> None:
+    """Move the pages in use to the bottom of the pools; live [1] receives how many there are."""
+    _pools(zha_pages_get_desc(handle), K, V)
+    _expect(live, "live", 1, _I32)
+    _here(handle, K, V, live)
+    _check(lib().zha_pages_compact(handle, _ptr(K), _ptr(V), _ptr(live), _stream(stream)), "zha_pages_compact")
+
+
+def zha_pages_gather(handle, K: torch.Tensor, V: torch.Tensor, seqs: torch.Tensor, K_out: torch.Tensor,
+                     V_out: torch.Tensor, stream=None) -> None:
+    """Copy sequences seqs [n] into a dense cache [n, kv_heads, capacity, head_dim]."""
+    d = zha_pages_get_desc(handle)
+    _pools(d, K, V)
+    n = _slots(seqs, "seqs")
+    cap = _rows(d, n, K_out, V_out, "_out")
+    _here(handle, K, V, seqs, K_out, V_out)
+    _check(lib().zha_pages_gather(handle, _ptr(K), _ptr(V), _ptr(seqs), n, _ptr(K_out), _ptr(V_out), cap,
+                                  _stream(stream)), "zha_pages_gather")
+
+
+def zha_pages_check(handle, stream=None) -> int:
+    return int(lib().zha_pages_check(handle, _stream(stream)))
+
+
+def zha_prefix_attn_scratch_bytes(handle, batch: int, q_heads: int, nq: int, prefix_tokens: int) -> int:
+    return int(lib().zha_prefix_attn_scratch_bytes(handle, batch, q_heads, nq, prefix_tokens))
+
+
+def zha_prefix_attn_decode(handle, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seqs: torch.Tensor,
+                           prefix_seq: int, prefix_tokens: int, causal: bool, scale: float, O: torch.Tensor,
+                           scratch: torch.Tensor, stream=None) -> None:
+    """Attention of slots seqs [batch] whose first prefix_tokens tokens are prefix_seq's pages."""
+    d = zha_pages_get_desc(handle)
+    if Q.dim() != 4 or Q.shape[3] != d.head_dim:
+        raise ValueError(f"Q: shape {tuple(Q.shape)}, expected [batch, q_heads, nq, {d.head_dim}]")
+    B, Hq, nq, _ = Q.shape
+    _expect(Q, "Q", Q.numel(), _OUT)
+    _expect(O, "O", Q.numel(), _OUT)
+    _pools(d, K, V)
+    _slots(seqs, "seqs", B)
+    _here(handle, Q, K, V, seqs, O, scratch)
+    _check(lib().zha_prefix_attn_decode(handle, _ptr(Q), dtype_code(Q.dtype), B, Hq, nq, _ptr(K), _ptr(V),
+                                        _ptr(seqs), prefix_seq, prefix_tokens, int(causal), scale, _ptr(O),
+                                        dtype_code(O.dtype), _ptr(scratch),
+                                        scratch.numel() * scratch.element_size(), _stream(stream)),
+           "zha_prefix_attn_decode")
+
+
+# ---------------------------------------------------------------- convenience owners
 
 class Tree:
     """A tree set over a [batch, kv_heads, capacity, head_dim] cache, with its workspace."""
@@ -604,3 +821,108 @@ class Tree:
 
     def check(self, stream=None) -> int:
         return zha_tree_check(self.handle, stream)
+
+
+def _allocating(stream):
+    """Context in which new tensors belong to `stream` (a torch stream, a cudaStream_t or None: the
+    current one), so that their memory is not reused before that stream is done with them."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+class Pages:
+    """A paged cache over pools K, V [num_pages, kv_heads, page_tokens, head_dim], with its workspace.
+
+    Slot lists are int32 device tensors.  table, lens and refs are views of the cache's state on
+    the device (to read; load() replaces it)."""
+
+    def __init__(self, kv_heads: int, head_dim: int, page_tokens: int, num_pages: int, max_seqs: int,
+                 max_seq_pages: int, kv_dtype: torch.dtype, device="cuda", stream=None):
+        self.desc = zha_pages_desc(kv_heads, head_dim, page_tokens, num_pages, max_seqs, max_seq_pages,
+                                   dtype_code(kv_dtype))
+        self.handle = None
+        nbytes = zha_pages_workspace_bytes(self.desc)
+        if nbytes == 0:
+            raise ZhaError(ZHA_ERR_UNSUPPORTED, "zha_pages_workspace_bytes")
+        with _allocating(stream):
+            self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        with torch.cuda.device(self.workspace.device):
+            self.handle = zha_pages_init(self.desc, self.workspace, stream)
+        self.table = self._view(zha_pages_table(self.handle), max_seqs * max_seq_pages).view(max_seqs, max_seq_pages)
+        self.lens = self._view(zha_pages_lens(self.handle), max_seqs)
+        self.refs = self._view(zha_pages_refs(self.handle), num_pages)
+
+    def _view(self, address: int, n: int) -> torch.Tensor:
+        at = address - self.workspace.data_ptr()
+        return self.workspace[at:at + 4 * n].view(torch.int32)
+
+    def close(self):
+        if self.handle is not None:
+            zha_pages_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    @property
+    def launches(self) -> int:
+        return zha_pages_launch_count(self.handle)
+
+    def pools(self) -> tuple[torch.Tensor, torch.Tensor]:
+        """New, uninitialised K and V pools of the cache's shape and type."""
+        d = self.desc
+        shape = (d.num_pages, d.kv_heads, d.page_tokens, d.head_dim)
+        return tuple(torch.empty(shape, dtype=_TORCH_DT[d.kv_dtype], device=self.workspace.device) for _ in "KV")
+
+    def load(self, table: torch.Tensor, lens: torch.Tensor, stream=None):
+        zha_pages_load(self.handle, table, lens, stream)
+
+    def append(self, K: torch.Tensor, V: torch.Tensor, seqs: torch.Tensor, K_new: torch.Tensor, V_new: torch.Tensor,
+               counts: torch.Tensor | None = None, stream=None):
+        zha_pages_append(self.handle, K, V, seqs, K_new, V_new, counts, stream)
+
+    def fork(self, K: torch.Tensor, V: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, stream=None):
+        zha_pages_fork(self.handle, K, V, src, dst, stream)
+
+    def copy(self, K: torch.Tensor, V: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, stream=None,
+             source: "Pages | None" = None, K_from: torch.Tensor | None = None, V_from: torch.Tensor | None = None):
+        """Copy sequences src of `source` (pools K_from, V_from; default: this cache) to empty slots dst."""
+        if source is None:
+            source, K_from, V_from = self, K, V
+        zha_pages_copy(source.handle, K_from, V_from, self.handle, K, V, src, dst, stream)
+
+    def free(self, seqs: torch.Tensor, stream=None):
+        zha_pages_free(self.handle, seqs, stream)
+
+    def compact(self, K: torch.Tensor, V: torch.Tensor, stream=None) -> torch.Tensor:
+        """Move the pages in use to the bottom of the pools; returns how many there are (device)."""
+        with _allocating(stream):
+            live = torch.empty((), dtype=torch.int32, device=self.workspace.device)
+        zha_pages_compact(self.handle, K, V, live, stream)
+        return live
+
+    def gather(self, K: torch.Tensor, V: torch.Tensor, seqs: torch.Tensor, K_out: torch.Tensor, V_out: torch.Tensor,
+               stream=None):
+        zha_pages_gather(self.handle, K, V, seqs, K_out, V_out, stream)
+
+    def attend(self, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: float, seqs: torch.Tensor,
+               prefix_seq: int = 0, prefix_tokens: int = 0, causal: bool = False,
+               out_dtype: torch.dtype = torch.bfloat16, O: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Attention of Q [batch, q_heads, nq, head_dim] over slots seqs [batch], whose first
+        prefix_tokens tokens are the pages of slot prefix_seq."""
+        need = zha_prefix_attn_scratch_bytes(self.handle, Q.shape[0], Q.shape[1], Q.shape[2], prefix_tokens)
+        with _allocating(stream):
+            if O is None:
+                O = torch.empty(Q.shape, dtype=out_dtype, device=Q.device)
+            scratch = torch.empty(max(need, 16), dtype=torch.uint8, device=Q.device)
+        zha_prefix_attn_decode(self.handle, Q, K, V, seqs, prefix_seq, prefix_tokens, causal, scale, O, scratch, stream)
+        return O
+
+    def check(self, stream=None) -> int:
+        return zha_pages_check(self.handle, stream)
