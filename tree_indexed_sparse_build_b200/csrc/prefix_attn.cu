@@ -362,7 +362,7 @@ cudaError_t launch_fp32(const PrefixArgs& a, cudaStream_t s) {
 template <int D>
 cudaError_t launch_fp32_types(const PrefixArgs& a, zha_dtype q, zha_dtype kv, cudaStream_t s) {
   if (q == ZHA_F32) return kv == ZHA_F32 ? launch_fp32<D, float, float>(a, s) : launch_fp32<D, float, uint16_t>(a, s);
-  return kv == ZHA_F32 ? launch_fp32<D, uint16_t, float>(a, s) : launch_fp32<D, uint16_t, uint16_t>(a, s);
+  return launch_fp32<D, uint16_t, float>(a, s);
 }
 
 template <int D>
@@ -414,7 +414,9 @@ bool plan(const zha_pages* p, int batch, int q_heads, int nq, long long prefix, 
   return true;
 }
 
-bool tensor_path(const zha_pages* p, zha_dtype q) { return false; }
+// bf16 against bf16 runs on the tensor cores at any size: their tiles cost less than the bytes even when
+// a tile is mostly empty.
+bool tensor_path(const zha_pages* p, zha_dtype q) { return q == ZHA_BF16 && p->desc.kv_dtype == ZHA_BF16; }
 
 struct Scratch {
   size_t cum, ml, acc, bytes;
@@ -486,8 +488,9 @@ zha_status zha_prefix_attn_decode(const zha_pages* p, const void* d_Q, zha_dtype
   a.wait_cycles = p->wait_limit > 0 ? p->wait_limit : kCopyWaitCycles;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int d = p->desc.head_dim;
-  cudaError_t e = d == 64 ? launch_fp32_types<64>(a, q_dtype, p->desc.kv_dtype, s)
-                          : launch_fp32_types<128>(a, q_dtype, p->desc.kv_dtype, s);
+  cudaError_t e = tensor    ? launch_prefix_tc(p, a, d, o_dtype == ZHA_F32, s)
+                  : d == 64 ? launch_fp32_types<64>(a, q_dtype, p->desc.kv_dtype, s)
+                            : launch_fp32_types<128>(a, q_dtype, p->desc.kv_dtype, s);
   if (e == cudaSuccess) e = d == 64 ? launch_join<64>(a, o_dtype, s) : launch_join<128>(a, o_dtype, s);
   const_cast<zha_pages*>(p)->launches += 2;  // the handle is logically const
   return e == cudaSuccess ? ZHA_OK : ZHA_ERR_CUDA;
