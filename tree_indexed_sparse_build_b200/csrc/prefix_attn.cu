@@ -62,7 +62,7 @@ struct Fp32Tile {
 
     // row r of the tile -> (sequence, row within it)
     auto place = [&](int r, int* b, int* rem) {
-      if (g.own) {
+      if (g.kind == kOwn) {
         *b = g.b;
         *rem = g.tile * s.own_tile + r;
         return *rem < s.rows && r < s.own_tile;
@@ -108,12 +108,8 @@ struct Fp32Tile {
 #pragma unroll
       for (int c = 0; c < 4 * C; ++c) acc[i][c] = 0.f;
     }
-    int slot = s.prefix_seq, first = 0, end = s.prefix;
-    if (g.own) {
-      end = prefix_len(a, g.b, &slot);
-      first = s.prefix;
-    }
-    const int* pages = a.v.table + (size_t)slot * a.v.width;
+    const int first = g.kind == kOwn ? s.prefix : 0, end = g.len;
+    const int* pages = a.v.table + (size_t)g.pages * a.v.width;
     const TKV* K = static_cast<const TKV*>(a.K);
     const TKV* V = static_cast<const TKV*>(a.V);
 
@@ -210,14 +206,14 @@ struct Fp32Tile {
 template <int D, typename TQ, typename TKV>
 __global__ void __launch_bounds__(kThreads, 2) fp32_kernel(const __grid_constant__ PrefixArgs a) {
   extern __shared__ float smem[];
-  __shared__ long long share[kThreads / 32 + 4];
+  __shared__ int share[kThreads / 32 + 4];
   pdl_wait();
   pdl_release();
   using Tile = Fp32Tile<D, TQ, TKV>;
   Walk w = find_share(a, blockIdx.x, kThreads, share);
   Segment g;
   while (w.next(a, blockIdx.x, &g)) {
-    if ((g.own ? a.s.own_tile : a.s.prefix_tile) == 16)
+    if ((g.kind == kOwn ? a.s.own_tile : a.s.prefix_tile) == 16)
       Tile::template segment<16>(a, g, smem);
     else
       Tile::template segment<64>(a, g, smem);
@@ -229,10 +225,6 @@ __global__ void __launch_bounds__(kThreads, 2) fp32_kernel(const __grid_constant
 // One CTA per output row: its warps take the row's partial results in turn, rescale by the
 // maxima and add (fp32); the order is fixed, so the result does not depend on timing.
 constexpr int kJoinWarps = 8;
-
-struct Part {
-  float m, l;
-};
 
 template <int D>
 struct Joined {
@@ -252,16 +244,10 @@ struct Joined {
   }
 };
 
-// The CTA whose share holds cost position x.
-__device__ __forceinline__ int cta_of(long long x, long long T, int ctas) { return (int)(((x + 1) * ctas - 1) / T); }
-
-// Key tiles of an item (first at cost `start`, `n` of cost w each) in CTA c's share.
-__device__ __forceinline__ int tiles_in(long long start, int n, int w, int c, long long T, int ctas) {
-  const long long lo = c * T / ctas, hi = (c + 1) * T / ctas;
-  long long t0 = lo > start ? (lo - start + w - 1) / w : 0;
-  long long t1 = hi > start ? (hi - start + w - 1) / w : 0;
-  if (t1 > n) t1 = n;
-  return t1 > t0 ? (int)(t1 - t0) : 0;
+// The CTA whose share of T holds key tile x.
+__device__ __forceinline__ int cta_of(int x, int T, int ctas) {
+  const int each = T / ctas, more = T - each * ctas, bent = more * (each + 1);
+  return x < bent ? x / (each + 1) : more + (x - bent) / each;
 }
 
 template <int D, typename TO>
@@ -275,7 +261,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   const int rem = (int)(at % s.rows), head = (int)(at / s.rows % s.heads), b = (int)(at / s.rows / s.heads);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int group = s.heads * s.own_tiles;
-  const long long T = s.prefix_cost + a.cum[s.batch] * group;
+  const int T = s.prefix_total + a.cum[s.batch] * group;
   Joined<D> sum;
   auto take = [&](long long row) {
     const float2 x = a.ml[row];
@@ -289,6 +275,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     }
     sum.add(x.x, x.y, y);
   };
+  // the partial results of the segments of an item of n key tiles at `start`: `parts` rows `step` apart
+  // of each stream that took part
+  auto item = [&](int start, int n, int streams, int parts, long long slot0, int slot_rows, int step) {
+    const int c0 = cta_of(start, T, s.ctas), c1 = cta_of(start + n - 1, T, s.ctas);
+    const int each = streams * parts;
+    for (int i = warp; i < (c1 - c0 + 1) * each; i += kJoinWarps) {
+      const int c = c0 + i / each, k = i % each;
+      const int tiles = min(start + n, share_start(c + 1, T, s.ctas)) - max(start, share_start(c, T, s.ctas));
+      if (tiles <= k / parts) continue;
+      take(slot0 + (long long)c * slot_rows + k * step);
+    }
+  };
   if (s.prefix > 0) {
     int rt, r;
     if (s.seqs_per_tile) {
@@ -298,30 +296,23 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
       rt = b * s.tiles_per_seq + rem / s.prefix_tile;
       r = rem % s.prefix_tile;
     }
-    const int pair = rt < 2 * s.duals ? rt >> 1 : rt - s.duals;
-    const bool dual = pair < s.duals;
-    const int w = dual ? s.dual_cost : 1;
-    const long long one = (long long)s.prefix_keys * s.dual_cost;
-    const long long start = head * s.head_cost + (dual ? pair * one : s.duals * one + (long long)(pair - s.duals) * s.prefix_keys);
-    const long long slot = (long long)head * s.pairs + pair;
-    const int c0 = cta_of(start, T, s.ctas), c1 = cta_of(start + (long long)(s.prefix_keys - 1) * w, T, s.ctas);
-    const int streams = dual ? 1 : s.streams;
-    for (int i = warp; i < (c1 - c0 + 1) * streams; i += kJoinWarps) {
-      const int c = c0 + i / streams, st = i % streams;
-      if (tiles_in(start, s.prefix_keys, w, c, T, s.ctas) <= st) continue;
-      take((slot + c) * s.prefix_slot_rows + (dual ? (rt & 1) * s.prefix_tile : st * s.prefix_tile) + r);
+    if (rt < 2 * s.duals) {
+      const int x = head * s.duals + (rt >> 1);
+      item(x * s.prefix_keys, s.prefix_keys, 1, 1, (long long)x * s.dual_slot_rows + (rt & 1) * s.prefix_tile + r, s.dual_slot_rows, 0);
+    } else {
+      const int x = head * s.singles + rt - 2 * s.duals;
+      item(s.dual_total + x * s.prefix_keys, s.prefix_keys, s.streams, s.prefix_parts, s.single_slot0 + (long long)x * s.single_slot_rows + r, s.single_slot_rows,
+           s.single_slot_rows / (s.streams * s.prefix_parts));
     }
   }
-  const int n = (int)(a.cum[b + 1] - a.cum[b]);
+  int slot;
+  const int len = prefix_len(a, b, &slot);
+  const int n = own_key_tiles(s, len);
   if (n > 0) {
-    const int item = head * s.own_tiles + rem / s.own_tile, r = rem % s.own_tile;
-    const long long start = s.prefix_cost + a.cum[b] * group + (long long)item * n;
-    const int c0 = cta_of(start, T, s.ctas), c1 = cta_of(start + n - 1, T, s.ctas);
-    for (int i = warp; i < (c1 - c0 + 1) * s.streams; i += kJoinWarps) {
-      const int c = c0 + i / s.streams, st = i % s.streams;
-      if (tiles_in(start, n, 1, c, T, s.ctas) <= st) continue;
-      take(s.own_slot0 + ((long long)b * group + item + c) * s.own_slot_rows + st * (s.own_slot_rows / s.streams) + r);
-    }
+    const int x = head * s.own_tiles + rem / s.own_tile;
+    item(s.prefix_total + a.cum[b] * group + x * n, n, s.streams, s.own_parts,
+         s.own_slot0 + ((long long)b * group + x) * s.own_slot_rows + rem % s.own_tile, s.own_slot_rows,
+         s.own_slot_rows / (s.streams * s.own_parts));
   }
   if (lane == 0) {
     s_m[warp] = sum.m;
@@ -334,8 +325,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   Joined<D> all;
 #pragma unroll
   for (int i = 0; i < kJoinWarps; ++i) all.add(s_m[i], s_l[i], &s_acc[i][lane * (D / 32)]);
-  int slot;
-  const bool sees = tokens_seen(s, prefix_len(a, b, &slot), rem % s.nq) > 0;
+  const bool sees = tokens_seen(s, len, rem % s.nq) > 0;
   const bool lost = (*a.v.err & kDevErrTimeout) != 0;
   TO* O = static_cast<TO*>(a.O) + at * D + lane * (D / 32);
 #pragma unroll
@@ -392,25 +382,38 @@ bool plan(const zha_pages* p, int batch, int q_heads, int nq, long long prefix, 
   // fp32: 16 rows at a time where there are no more, else 64 (the arithmetic is per tile row)
   s->prefix_tile = tensor ? 128 : rows * batch <= 16 ? 16 : 64;
   s->own_tile = tensor ? 128 : rows <= 16 ? 16 : 64;
+  int row_tiles;
   if (rows <= s->prefix_tile) {
     s->seqs_per_tile = s->prefix_tile / (int)rows;
-    s->row_tiles = ceil_div(batch, s->seqs_per_tile);
+    row_tiles = ceil_div(batch, s->seqs_per_tile);
   } else {
     s->tiles_per_seq = ceil_div(rows, s->prefix_tile);
-    s->row_tiles = batch * s->tiles_per_seq;
+    row_tiles = batch * s->tiles_per_seq;
   }
-  s->duals = tensor ? s->row_tiles / 2 : 0;
-  s->pairs = s->row_tiles - s->duals;
+  s->duals = tensor ? row_tiles / 2 : 0;
+  s->singles = row_tiles - 2 * s->duals;
   s->streams = tensor ? 2 : 1;
   s->own_tiles = ceil_div(rows, s->own_tile);
   s->prefix_keys = ceil_div(prefix, s->tile_keys);
-  s->dual_cost = 2;
+  // up to 32 rows fill one warp's lanes of TMEM; the tensor kernel then lets each of a stream's four
+  // warps weigh a quarter of the keys and leaves four partial results
+  s->prefix_parts = tensor && rows * batch <= 32 ? 4 : 1;
+  s->own_parts = tensor && rows <= 32 ? 4 : 1;
   s->ctas = tensor ? p->sms : 2 * p->sms;
-  s->head_cost = ((long long)s->duals * s->dual_cost + (s->pairs - s->duals)) * s->prefix_keys;
-  s->prefix_cost = s->head_cost * heads;
-  s->prefix_slot_rows = tensor ? 2 * s->prefix_tile : s->prefix_tile;
-  s->own_slot_rows = s->streams * (int)(rows < s->own_tile ? rows : s->own_tile);
-  s->own_slot0 = prefix > 0 ? ((long long)s->pairs * heads + s->ctas) * s->prefix_slot_rows : 0;
+  // all key tiles, sequences as long as they may be, are counted in 31 bits
+  const long long most = (long long)p->desc.max_seq_pages * p->desc.page_tokens;
+  if ((long long)heads * row_tiles * s->prefix_keys +
+          (long long)batch * heads * s->own_tiles * ceil_div(most, s->tile_keys) > 0x7fffffffLL)
+    return false;
+  s->dual_total = heads * s->duals * s->prefix_keys;
+  s->prefix_total = s->dual_total + heads * s->singles * s->prefix_keys;
+  s->dual_slot_rows = 2 * s->prefix_tile;
+  const int single_rows = s->prefix_parts == 4 ? (int)rows * batch : s->prefix_tile;
+  s->single_slot_rows = s->streams * s->prefix_parts * single_rows;
+  s->own_slot_rows = s->streams * s->own_parts * (int)(rows < s->own_tile ? rows : s->own_tile);
+  const long long shared = prefix > 0;
+  s->single_slot0 = shared && s->duals ? ((long long)s->duals * heads + s->ctas) * s->dual_slot_rows : 0;
+  s->own_slot0 = s->single_slot0 + (shared && s->singles ? ((long long)s->singles * heads + s->ctas) * s->single_slot_rows : 0);
   return true;
 }
 
@@ -427,7 +430,7 @@ Scratch scratch_of(const zha_pages* p, const PrefixShape& s) {
       s.own_slot0 + ((long long)s.batch * s.heads * s.own_tiles + s.ctas) * s.own_slot_rows;
   Scratch x;
   x.cum = 0;
-  x.ml = ((size_t)(s.batch + 1) * 8 + 255) / 256 * 256;
+  x.ml = ((size_t)(s.batch + 1) * 4 + 255) / 256 * 256;
   x.acc = x.ml + ((size_t)rows * 8 + 255) / 256 * 256;
   x.bytes = x.acc + (size_t)rows * p->desc.head_dim * 4;
   return x;
@@ -480,7 +483,7 @@ zha_status zha_prefix_attn_decode(const zha_pages* p, const void* d_Q, zha_dtype
   a.K = d_K;
   a.V = d_V;
   a.seqs = d_seqs;
-  a.cum = reinterpret_cast<long long*>(base + x.cum);
+  a.cum = reinterpret_cast<int*>(base + x.cum);
   a.ml = reinterpret_cast<float2*>(base + x.ml);
   a.acc = reinterpret_cast<float*>(base + x.acc);
   a.O = d_O;

@@ -3,18 +3,25 @@
 // S = Q K^T and O += P V of a tile of 128 rows against 128 keys are tcgen05 MMAs with
 // accumulators in TMEM.  A CTA holds two streams, each with its S (128 columns, overwritten
 // in place by P) and its O: while one stream's 128 threads (one row each) form its weights,
-// the other's MMAs run.  An item of two row tiles runs them as the two streams over the same
-// keys, which halves the key and value traffic; an item of one row tile gives its streams alternate
-// key tiles, and the join adds the two results.
+// the other's MMAs run.  A dual item's two row tiles are the two streams over the same keys, which
+// halves the key and value traffic.  The key tiles of all other segments of a CTA's share are dealt
+// to the streams in turn, across segments, so that a run of short sequences keeps both busy; the
+// join adds what the two streams leave of a segment.
 //
 //   warps 0-3, 4-7  stream 0, 1: maximum, exp2, sum, P; correction and output of O
 //   warp 8          TMA: queries, and keys and values page by page into a ring
-//   warp 9          MMA issue (one lane) and TMEM
+//   warp 9          MMA issue (one lane), for both streams: an issuer each let the streams fall into
+//                   step, so that MMAs and weights took turns instead of overlapping
+//   warp 10         TMEM; warps 10 and 11 give their registers to the streams' warps
+//
+// Up to 32 rows fill one warp's lanes.  Then the queries are loaded four times, into the lanes of each
+// warp, and each weighs a quarter of the keys (P is zero elsewhere): a fourth of the
+// latency per tile, for four partial results instead of one.
 //
 // The maximum that weights refer to moves only when a score exceeds it by more than 8 in
 // base 2: weights then stay below 2^8, which costs no accuracy in floating point, and O is rarely
 // rescaled.  Rows of a page past the sequence may hold anything: their scores are replaced, and
-// their rows of V zeroed in shared memory, because 0 times NaN is NaN.
+// the rows of V that an MMA step still touches are zeroed in shared memory, because 0 times NaN is NaN.
 //
 // Every wait is bounded; one that runs out sets an error that makes all warps leave, the
 // producer waiting (bounded) for its loads and the issuer for its MMAs.
@@ -28,8 +35,9 @@ using namespace zha;
 namespace {
 
 constexpr int kRows = 128, kKeys = 128;
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kTmemCols = 512;
+constexpr int kByFma = 6;     // of 16 pairs of weights, those whose exp2 the FMA pipes compute
 constexpr float kSlack = 8.f;  // base-2 growth of the maximum that is let pass
 
 struct TcMaps {
@@ -54,21 +62,36 @@ struct Tc {
 
 struct Bars {
   uint64_t full[10], empty[10], q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2], o_free[2], drain;
+  int2 meta[10];  // of a ring place: its keys, and PlaceFlags
   uint32_t tmem;
   int gone;  // a wait ran out
-  long long share[kThreads / 32 + 4];
+  int share[kThreads / 32 + 4];
 };
 static_assert(sizeof(Bars) <= 1024, "the barriers' page");
 
+// What the issuer has to know of a ring place, written by the loader.
+enum PlaceFlags {
+  kFirst = 1,     // keys: the segment's first tile; values: its stream's first of the segment
+  kLast = 2,      // .. last
+  kPaired = 4,    // a dual tile: both streams use the place
+  kLoneNext = 8,  // a dual tile that no dual tile follows
+  kEnd = 16       // no tile: the share is done
+};
+
+// Bounded waits on the barriers of one CTA.  A whole warp waits, and all of its lanes get the same answer:
+// what follows (TMEM accesses, MMA issue) needs the warp to stay together, also when it gives up.
 struct Waiter {
   unsigned* err;
   volatile int* gone;
-  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity, long long limit) const {
-    if (limit >= kPollWaitBelow && mbar_try_wait(bar, parity)) return true;
+
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity, long long limit = kCopyWaitCycles) const {
+    constexpr unsigned all = 0xffffffffu;
+    const bool poll = limit < kPollWaitBelow;  // a test's
+    if (!poll && __all_sync(all, mbar_try_wait(bar, parity))) return true;
     const long long t0 = clock64();
-    while (!(limit < kPollWaitBelow ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity))) {
-      if (*gone) return false;
-      if (clock64() - t0 > limit) {
+    while (!__all_sync(all, poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity))) {
+      if (__any_sync(all, *gone != 0)) return false;
+      if (__any_sync(all, clock64() - t0 > limit)) {
         atomicOr(err, kDevErrTimeout);
         *gone = 1;
         return false;
@@ -78,22 +101,496 @@ struct Waiter {
   }
 };
 
-// Place in the ring, from the segment's first, of the keys and values of tile j of n.
-__device__ __forceinline__ int k_at(bool dual, int j) { return dual ? 2 * j : j ? 2 * j - 1 : 0; }
-__device__ __forceinline__ int v_at(bool dual, int j, int n) { return dual ? 2 * j + 1 : j < n - 1 ? 2 * j + 2 : 2 * n - 1; }
+// The key tiles of a CTA's share, one after the other.
+struct Tiles {
+  Walk w;
+  Segment g;
+  int t;
+  bool any;
+  __device__ __forceinline__ Tiles(const PrefixArgs& a, const Walk& from, int cta) : w(from) {
+    any = w.next(a, cta, &g);
+    t = g.t0;
+  }
+  __device__ __forceinline__ bool dual() const { return g.kind == kDual; }
+  __device__ __forceinline__ int k0(const PrefixArgs& a) const { return (g.kind == kOwn ? a.s.prefix : 0) + t * kKeys; }
+  __device__ __forceinline__ int keys(const PrefixArgs& a) const { return min(kKeys, g.len - k0(a)); }
+  __device__ __forceinline__ void step(const PrefixArgs& a, int cta) {
+    if (++t == g.t1) {
+      any = w.next(a, cta, &g);
+      t = g.t0;
+    }
+  }
+};
+
+// A place in the ring and how often the ring has gone round.
+template <int STAGES>
+struct Place {
+  int stage = 0;
+  uint32_t round = 0, index = 0;
+  __device__ __forceinline__ void add(int n) {  // n <= STAGES
+    index += n;
+    stage += n;
+    if (stage >= STAGES) {
+      stage -= STAGES;
+      round ^= 1;
+    }
+  }
+};
+
+template <int REGS>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS)); }
+template <int REGS>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS)); }
+
+// The kernel launches with 168 registers a thread: 384 x 168 = 128 x (2 x 192 + 120).
+constexpr int kStreamRegs = 192, kOtherRegs = 120;
+
+// ---- warp 8
+
+template <int D>
+struct Loader {
+  using C = Tc<D>;
+  const TcArgs& args;
+  const PrefixArgs& a;
+  Bars& bars;
+  const Waiter& wait;
+  uint32_t q_smem, kv_smem;
+  int lane, per_tile, chunk, half;
+  bool mine;
+  Place<C::kStages> at;
+  uint32_t qc = 0;  // query tiles loaded
+
+  __device__ __forceinline__ Loader(const TcArgs& x, Bars& b, const Waiter& w, uint32_t q, uint32_t kv)
+      : args(x), a(x.a), bars(b), wait(w), q_smem(q), kv_smem(kv), lane(threadIdx.x & 31) {
+    per_tile = kKeys >> args.chunk_shift;
+    chunk = lane % per_tile;
+    half = lane / per_tile;
+    mine = lane < per_tile * (D / 64);
+  }
+
+  // Row tile `rt` of g to the next query buffer.
+  __device__ __forceinline__ bool queries(const Segment& g, int rt) {
+    const PrefixShape& s = a.s;
+    const int buf = qc & 1;
+    if (!wait(&bars.q_empty[buf], ((qc >> 1) & 1) ^ 1)) return false;
+    const int copies = g.kind == kOwn ? s.own_parts : g.kind == kSingle ? s.prefix_parts : 1;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&bars.q_full[buf], copies * (g.kind == kOwn ? args.q_own_bytes : args.q_prefix_bytes));
+      for (int i = 0; i < copies; ++i)
+        for (int h = 0; h < D / 64; ++h) {
+          const uint32_t dst = q_smem + buf * C::kTile + h * C::kHalf + i * 32 * 128;
+          if (g.kind == kOwn)
+            tma_load4(dst, &args.maps.q_own, h * 64, g.tile * s.own_tile, g.head, g.b, &bars.q_full[buf]);
+          else if (s.seqs_per_tile)
+            tma_load4(dst, &args.maps.q_prefix, h * 64, 0, g.head, rt * s.seqs_per_tile, &bars.q_full[buf]);
+          else
+            tma_load4(dst, &args.maps.q_prefix, h * 64, rt % s.tiles_per_seq * s.prefix_tile, g.head, rt / s.tiles_per_seq,
+                      &bars.q_full[buf]);
+        }
+    }
+    __syncwarp();
+    ++qc;
+    return true;
+  }
+
+  // Page of this lane's part of the key tile (a bad id becomes one past the pool, which reads as zeros).
+  __device__ __forceinline__ int page_of(const Tiles& x) const {
+    const int token = x.k0(a) + (chunk << args.chunk_shift);
+    if (!mine || token >= x.g.len) return -1;
+    const int id = a.v.table[(size_t)x.g.pages * a.v.width + (token >> a.v.shift)];
+    if ((unsigned)id < (unsigned)a.v.num_pages) return id;
+    atomicOr(a.v.err, kDevErrBadSeq);
+    return a.v.num_pages;
+  }
+
+  // Order of the ring: K0 V0 K1 V1 .. for dual tiles, which both streams read together, then
+  // K0 K1 V0 K2 V1 .., tile x for stream x & 1; where the next K would be, a place that says that there is none.
+  __device__ __forceinline__ bool run(const Walk& walk, int cta) {
+    Tiles x(a, walk, cta);
+    int page = x.any ? page_of(x) : -1;
+    struct Place1 {
+      int head, k0, n, page, flags;
+    } now, before;
+    before = now = {0, 0, 0, -1, 0};
+    bool pending = false;  // the tile before still lacks its values
+    bool ended = false;
+    while (!ended) {
+      const bool any = x.any, dual = any && x.dual();
+      int k_flags = kEnd;
+      if (any) {
+        const int by = dual ? 1 : 2;
+        if (x.t == x.g.t0)
+          for (int i = 0; i < 1 + dual; ++i)
+            if (!queries(x.g, x.g.tile + i)) return false;
+        k_flags = (x.t == x.g.t0 ? kFirst : 0) | (x.t + 1 == x.g.t1 ? kLast : 0) | (dual ? kPaired : 0);
+        now = {x.g.head, x.k0(a), x.keys(a), page, dual ? kPaired : 0};
+        if (x.t < x.g.t0 + by) now.flags |= kFirst;
+        if (x.t + by >= x.g.t1) now.flags |= kLast;
+        x.step(a, cta);
+        if (x.any) page = page_of(x);
+        if (dual && !(x.any && x.dual())) now.flags |= kLoneNext;
+      } else {
+        ended = true;
+      }
+#pragma unroll 1
+      for (int values = 0; values < 2; ++values) {
+        if (values && !dual && !pending) break;
+        const bool here = !values || dual;  // this tile, or the one before
+        const int n = here ? now.n : before.n, k0 = here ? now.k0 : before.k0, head = here ? now.head : before.head;
+        const int id = here ? now.page : before.page, chunks = (n + args.chunk - 1) >> args.chunk_shift;
+        if (!wait(&bars.empty[at.stage], at.round ^ 1)) return false;
+        if (lane == 0) {
+          bars.meta[at.stage] = make_int2(n, values ? (here ? now.flags : before.flags) : k_flags);
+          if (values || any)
+            mbar_arrive_expect_tx(&bars.full[at.stage], chunks * args.chunk * D * 2);
+          else
+            mbar_arrive(&bars.full[at.stage]);
+        }
+        __syncwarp();
+        if (id >= 0 && (values || any))
+          tma_load3(kv_smem + at.stage * C::kTile + half * C::kHalf + (chunk << args.chunk_shift) * 128,
+                    values ? &args.maps.v : &args.maps.k, half * 64, k0 & (a.v.page - 1) & ~(args.chunk - 1),
+                    id * a.s.heads + head, &bars.full[at.stage]);
+        at.add(1);
+      }
+      pending = any && !dual;
+      before = now;
+    }
+    return true;
+  }
+};
+
+// ---- warp 9
+
+template <int D, bool WIDE>
+struct Issuer {
+  using C = Tc<D>;
+  const PrefixArgs& a;
+  Bars& bars;
+  const Waiter& wait;
+  uint32_t q_smem, kv_smem, tmem;
+
+  __device__ __forceinline__ Issuer(const TcArgs& x, Bars& b, const Waiter& w, uint32_t q, uint32_t kv, uint32_t t)
+      : a(x.a), bars(b), wait(w), q_smem(q), kv_smem(kv), tmem(t) {}
+
+  // One lane: S = queries in buffer `buf` times the keys in `stage`; then the barriers that wait for it.
+  __device__ __forceinline__ void scores(int st, int buf, int stage, int2 m) {
+    const uint32_t desc = same(mma_desc(128, (m.x + 15) & ~15, false)), d = same(tmem + st * 128);
+    const uint32_t q = same((q_smem + buf * C::kTile) >> 4), k = same((kv_smem + stage * C::kTile) >> 4);
+    if (elect_one()) {
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) {
+        const uint32_t off = (x / 4 * C::kHalf + x % 4 * 32) >> 4;
+        mma_ss(d, desc_of(q + off, 16), desc_of(k + off, 16), desc, x > 0);
+      }
+      mma_commit(&bars.s_full[st]);
+      if (!(m.y & kPaired) || st == 1) mma_commit(&bars.empty[stage]);
+      if (m.y & kLast) mma_commit(&bars.q_empty[buf]);
+    }
+    __syncwarp();
+  }
+
+  // One lane: O (+)= P times the values in `stage`; then the barriers that wait for it.
+  __device__ __forceinline__ void values(int st, int stage, int2 m) {
+    constexpr uint32_t desc = mma_desc(128, D, true);
+    const uint32_t v = same((kv_smem + stage * C::kTile) >> 4), o = same(tmem + 256 + st * D), w = same(tmem + st * 128);
+    const int steps = same((m.x + 15) / 16);
+    const bool add = same(!(m.y & kFirst));
+    if (elect_one()) {
+#pragma unroll
+      for (int x = 0; x < kKeys / 16; ++x) {
+        if (x >= steps) break;
+        mma_ts(o, w + x * 8, desc_of(v + x * 128, C::kHalf), desc, add || x > 0);
+        if (WIDE) mma_ts(o, w + 64 + x * 8, desc_of(v + x * 128, C::kHalf), desc, true);
+      }
+      if (!(m.y & kPaired) || st == 1) mma_commit(&bars.empty[stage]);
+      if (m.y & kLast) mma_commit(&bars.o_full[st]);
+    }
+    __syncwarp();
+  }
+
+  // The place of a stream's next keys, or of none.
+  __device__ __forceinline__ bool look(const Place<C::kStages>& kp, uint32_t qc, int st, int2* k) {
+    *k = bars.meta[kp.stage];
+    const uint32_t q = qc + (k->y & kPaired ? st : 0);
+    return !(k->y & kFirst) || wait(&bars.q_full[q & 1], (q >> 1) & 1, a.wait_cycles);
+  }
+
+  // pairs: the share starts with a dual tile.
+  __device__ __forceinline__ bool run(bool pairs) {
+    Place<C::kStages> kp, vp;  // ring places of the next scores and values
+    vp.add(pairs ? 1 : 2);
+    uint32_t qc = 0, phase = 0;  // query tiles used up; bits 0, 1: phases of p_ready, 2, 3: of o_free
+    int todo = 0;                // tiles whose scores are issued and whose values are not
+    bool more = true, lone = false;
+    int st = 0;
+    for (int ahead = 2; more || todo; ahead -= ahead > 0, st ^= 1) {  // scores run two tiles ahead of values
+      int2 k;
+      bool seen = false;
+      if (ahead == 0) {
+        const int stage = vp.stage;
+        if (!wait(&bars.full[stage], vp.round, a.wait_cycles)) return false;
+        const int2 v = bars.meta[stage];
+        if ((v.y & kFirst) && !wait(&bars.o_free[st], ((phase >> (2 + st)) & 1) ^ 1)) return false;
+        if (v.y & kFirst) phase ^= 4u << st;
+        // while the weights are not there yet: the keys that follow, if they are
+        seen = more && __all_sync(0xffffffffu, mbar_test_wait(&bars.full[kp.stage], kp.round));
+        if (seen && !look(kp, qc, st, &k)) return false;
+        if (!wait(&bars.p_ready[st], (phase >> st) & 1)) return false;
+        phase ^= 1u << st;
+        tc_fence_after();
+        values(st, stage, v);
+        --todo;
+        // from the last dual tile's values to the first lone tile's: over K0 and K1
+        if (!(v.y & kPaired) || st == 1) vp.add(v.y & kLoneNext ? 3 : 2);
+      }
+      if (!more) continue;
+      if (!seen && (!wait(&bars.full[kp.stage], kp.round, a.wait_cycles) || !look(kp, qc, st, &k))) return false;
+      if (k.y & kEnd) {
+        more = false;
+        continue;
+      }
+      const bool paired = k.y & kPaired, done = !paired || st == 1;
+      scores(st, (qc + (paired ? st : 0)) & 1, kp.stage, k);
+      ++todo;
+      if (done) {
+        if (k.y & kLast) qc += paired ? 2 : 1;
+        kp.add(paired || lone ? 2 : 1);  // K1 comes right behind K0
+      }
+      lone = !paired;
+    }
+    return true;
+  }
+};
+
+// ---- warps 0 to 7
+
+template <int D, bool WIDE>
+struct Stream {
+  using C = Tc<D>;
+  const TcArgs& args;
+  const PrefixArgs& a;
+  Bars& bars;
+  const Waiter& wait;
+  char* ring;
+  uint32_t ts, to;  // this warp's lanes of S and O
+  int st, quarter, lane, r;
+  uint32_t ns = 0, no = 0;
+
+  __device__ __forceinline__ Stream(const TcArgs& x, Bars& b, const Waiter& w, char* kv, uint32_t tmem)
+      : args(x), a(x.a), bars(b), wait(w), ring(kv) {
+    const int warp = threadIdx.x >> 5;
+    lane = threadIdx.x & 31;
+    st = warp >> 2;
+    quarter = warp & 3;
+    r = quarter * 32 + lane;
+    ts = tmem + ((uint32_t)quarter << 21) + st * 128;
+    to = tmem + ((uint32_t)quarter << 21) + 256 + st * D;
+  }
+
+  float m, l;  // of this thread's row: what its weights refer to, their sum
+
+  // Weights of COLS keys: scores at S columns [col, col + COLS), of which the first lim count.  O is
+  // rescaled when the maximum moves (`fresh`: there is none yet).
+  template <int COLS>
+  __device__ __forceinline__ void weigh(int col, int lim, bool fresh) {
+    const float c = a.scale_log2;
+    uint32_t x[COLS];
+#pragma unroll
+    for (int q = 0; q < COLS / 32; ++q) tmem_ld32(x + 32 * q, ts + col + 32 * q);
+    tmem_wait_ld();
+    if (args.flip) {
+#pragma unroll
+      for (int k = 0; k < COLS; ++k) x[k] ^= 0x80000000u;
+    }
+    if (__any_sync(0xffffffffu, lim < COLS)) {
+#pragma unroll
+      for (int k = 0; k < COLS; ++k) x[k] = k < lim ? x[k] : 0xff800000u;
+    }
+    float t0 = __uint_as_float(x[0]), t1 = __uint_as_float(x[1]);
+#pragma unroll
+    for (int k = 2; k < COLS; k += 4) {
+      t0 = max3(t0, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+      if (k + 3 < COLS) t1 = max3(t1, __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+    }
+    const float top = fmaxf(t0, t1) * c;
+    float fix = 1.f;
+    if (m == -INFINITY) {
+      m = top;  // nothing of this row in O yet
+    } else if (top > m + kSlack) {
+      fix = exp2_approx(m - top);
+      m = top;
+    }
+    if (!fresh && __any_sync(0xffffffffu, fix != 1.f)) {
+      l *= fix;
+#pragma unroll
+      for (int q = 0; q < D / 16; ++q) {
+        uint32_t y[16];
+        tmem_ld16(y, to + 16 * q);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * fix);
+        tmem_st16(to + 16 * q, y);
+      }
+    }
+    const float off = m == -INFINITY ? 0.f : -m;
+    const uint64_t cc = pair(c, c), oo = pair(off, off);
+    uint64_t sum = pair(0.f, 0.f);
+#pragma unroll
+    for (int q = 0; q < COLS / 32; ++q) {
+      uint32_t hi[16], lo[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        float p0, p1;
+        const uint64_t e = fma2(pair(__uint_as_float(x[32 * q + 2 * k]), __uint_as_float(x[32 * q + 2 * k + 1])), cc, oo);
+        if (!WIDE && k % 16 < kByFma) {
+          exp2_by_fma(e, &p0, &p1);
+        } else {
+          split(e, &p0, &p1);
+          p0 = exp2_approx(p0);
+          p1 = exp2_approx(p1);
+        }
+        sum = add2(sum, pair(p0, p1));
+        hi[k] = pack_bf16(p0, p1);
+        if (WIDE) lo[k] = pack_bf16(p0 - __uint_as_float(hi[k] << 16), p1 - __uint_as_float(hi[k] & 0xffff0000u));
+      }
+      tmem_st16(ts + col / 2 + 16 * q, hi);
+      if (WIDE) tmem_st16(ts + 64 + col / 2 + 16 * q, lo);
+    }
+    float s0, s1;
+    split(sum, &s0, &s1);
+    l += s0 + s1;
+  }
+
+  // Zeros for the other warps' quarters of the keys.
+  __device__ __forceinline__ void clear_others() {
+    const uint32_t z[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (q != quarter) {
+        tmem_st16(ts + 16 * q, z);
+        if (WIDE) tmem_st16(ts + 64 + 16 * q, z);
+      }
+  }
+
+  // This stream's tiles j0, j0 + by, .. of a segment; v_at: ring place of tile 0's values, v_by from tile to tile.
+  __device__ __forceinline__ bool segment(const Segment& g, int j0, int by, uint32_t v_at, uint32_t v_by) {
+    const PrefixShape& s = a.s;
+    const int n = g.t1 - g.t0;
+    const int parts = g.kind == kOwn ? s.own_parts : g.kind == kSingle ? s.prefix_parts : 1;
+    const int row = parts == 4 ? lane : r;
+    const int first = g.kind == kOwn ? s.prefix : 0;
+    int b, rem, rows = kRows;  // rows that one partial result has
+    bool valid;
+    if (g.kind == kOwn) {
+      b = g.b;
+      rem = g.tile * s.own_tile + row;
+      valid = rem < s.rows;
+      rows = min(s.rows, s.own_tile);
+    } else {
+      const int rt = g.kind == kDual ? g.tile + st : g.tile;
+      if (s.seqs_per_tile) {
+        const int x = row / s.rows;
+        b = rt * s.seqs_per_tile + x;
+        rem = row - x * s.rows;
+        valid = x < s.seqs_per_tile && b < s.batch;
+      } else {
+        b = rt / s.tiles_per_seq;
+        rem = (rt - b * s.tiles_per_seq) * s.prefix_tile + row;
+        valid = rem < s.rows;
+      }
+      if (parts == 4) rows = s.rows * s.batch;
+    }
+    int row_end = 0;
+    if (valid) {
+      int slot;
+      const int len = g.kind == kOwn ? g.len : prefix_len(a, b, &slot);
+      row_end = min(g.len, tokens_seen(s, len, s.nq == 1 ? 0 : rem % s.nq));
+    }
+    const bool work = __any_sync(0xffffffffu, valid);
+    m = -INFINITY;
+    l = 0.f;
+    for (int j = j0; j < n; j += by) {
+      const int k0 = first + (g.t0 + j) * kKeys, left = min(kKeys, g.len - k0);
+      if (!wait(&bars.s_full[st], ns++ & 1)) return false;
+      tc_fence_after();
+      if (left & 15) {  // rows of V behind the sequence, up to the end of the last MMA's 16
+        const uint32_t p = v_at + v_by * j;
+        const int stage = p % C::kStages;
+        if (!wait(&bars.full[stage], (p / C::kStages) & 1)) return false;
+        if (r >= left && r < ((left + 15) & ~15)) {
+          char* v = ring + stage * C::kTile + r * 128;
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x)
+#pragma unroll
+            for (int y = 0; y < 8; ++y) *reinterpret_cast<uint4*>(v + x * C::kHalf + y * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
+      if (work) {
+        if (parts == 4) {
+          weigh<32>(32 * quarter, row_end - k0 - 32 * quarter, j == j0);
+          __syncwarp();
+          clear_others();
+        } else {
+          weigh<128>(0, row_end - k0, j == j0);
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.p_ready[st]);
+    }
+    if (!wait(&bars.o_full[st], no++ & 1)) return false;
+    tc_fence_after();
+    if (work) {
+      const int part = g.kind == kDual ? st : (j0 * parts + (parts == 4 ? quarter : 0));
+      const size_t out = (size_t)g.slot + part * rows + row;
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t y[32];
+        tmem_ld32(y, to + 32 * q);
+        tmem_wait_ld();
+        if (valid) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<uint4*>(a.acc + out * D + 32 * q + k) = make_uint4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+        }
+      }
+      if (valid) a.ml[out] = make_float2(m, l);
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.o_free[st]);
+    return true;
+  }
+
+  __device__ __forceinline__ bool run(Walk walk, int cta) {
+    Segment g;
+    uint32_t base = 0, x = 0;  // ring places of the dual tiles so far, single and own tiles so far
+    while (walk.next(a, cta, &g)) {
+      const bool dual = g.kind == kDual;
+      const int n = g.t1 - g.t0, j0 = dual ? 0 : (st ^ x) & 1;
+      if (j0 < n && !segment(g, j0, dual ? 1 : 2, base + (dual ? 1 : 2 * x + 2), 2)) return false;
+      if (dual)
+        base += 2 * n;
+      else
+        x += n;
+    }
+    return true;
+  }
+};
 
 template <int D, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__ TcArgs args) {
   extern __shared__ char raw[];
   using C = Tc<D>;
   const PrefixArgs& a = args.a;
-  const PrefixShape& s = a.s;
   char* base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
   Bars& bars = *reinterpret_cast<Bars*>(base + (2 + C::kStages) * C::kTile);
   const uint32_t q_smem = smem_addr(base), kv_smem = q_smem + 2 * C::kTile;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
   const Waiter wait{a.v.err, &bars.gone};
-  const long long bound = kCopyWaitCycles;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
@@ -112,324 +609,44 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     bars.gone = 0;
     fence_mbar_init();
   }
-  if (warp == 9) tmem_alloc(&bars.tmem, kTmemCols);
+  if (warp == 10) tmem_alloc(&bars.tmem, kTmemCols);
+  if (warp == 8 && lane < 4) prefetch_map(lane == 0 ? &args.maps.q_prefix : lane == 1 ? &args.maps.q_own : lane == 2 ? &args.maps.k : &args.maps.v);
   pdl_wait();
   pdl_release();
-  Walk walk = find_share(a, cta, kThreads, bars.share);
+  const Walk walk = find_share(a, cta, kThreads, bars.share);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars.tmem;
-  Segment g;
 
-  if (warp == 8) {
-    // ------------------------------------------------------------ loads
-    uint32_t at = 0, qc = 0;  // ring position, query tiles loaded
-    bool ok = true;
-    const int per_tile = kKeys >> args.chunk_shift;  // chunks
-    const int chunk = lane % per_tile, half = lane / per_tile;
-    const bool mine = lane < per_tile * (D / 64);
-    while (ok && walk.next(a, cta, &g)) {
-      const int tiles_q = g.dual ? 2 : 1;
-      for (int i = 0; ok && i < tiles_q; ++i, ++qc) {
-        const int buf = qc & 1;
-        ok = wait(&bars.q_empty[buf], ((qc >> 1) & 1) ^ 1, bound);
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&bars.q_full[buf], g.own ? args.q_own_bytes : args.q_prefix_bytes);
-          for (int h = 0; h < D / 64; ++h) {
-            const uint32_t dst = q_smem + buf * C::kTile + h * C::kHalf;
-            if (g.own) {
-              tma_load4(dst, &args.maps.q_own, h * 64, g.tile * s.own_tile, g.head, g.b, &bars.q_full[buf]);
-            } else {
-              const int rt = g.dual ? 2 * g.tile + i : g.tile + s.duals;
-              if (s.seqs_per_tile)
-                tma_load4(dst, &args.maps.q_prefix, h * 64, 0, g.head, rt * s.seqs_per_tile, &bars.q_full[buf]);
-              else
-                tma_load4(dst, &args.maps.q_prefix, h * 64, rt % s.tiles_per_seq * s.prefix_tile, g.head,
-                          rt / s.tiles_per_seq, &bars.q_full[buf]);
-            }
-          }
-        }
-        __syncwarp();
-      }
-      if (!ok) break;
-      int slot = s.prefix_seq, first = 0, end = s.prefix;
-      if (g.own) {
-        end = prefix_len(a, g.b, &slot);
-        first = s.prefix;
-      }
-      const int* row = a.v.table + (size_t)slot * a.v.width;
-      const int n = g.t1 - g.t0;
-      // page of this lane's chunk of tile j (a bad id becomes one past the pool: zeros)
-      auto page_of = [&](int j) {
-        const int t = first + (g.t0 + j) * kKeys + (chunk << args.chunk_shift);
-        if (j >= n || !mine || t >= end) return -1;
-        const int id = row[t >> a.v.shift];
-        if ((unsigned)id < (unsigned)a.v.num_pages) return id;
-        atomicOr(a.v.err, kDevErrBadSeq);
-        return a.v.num_pages;
-      };
-      auto load = [&](const CUtensorMap* map, int j, int page) {
-        const int stage = at % C::kStages;
-        if (!wait(&bars.empty[stage], ((at / C::kStages) & 1) ^ 1, bound)) return false;
-        const int k0 = first + (g.t0 + j) * kKeys;
-        const int chunks = min(per_tile, (end - k0 + args.chunk - 1) >> args.chunk_shift);
-        if (lane == 0) mbar_arrive_expect_tx(&bars.full[stage], chunks * args.chunk * D * 2);
-        __syncwarp();
-        if (page >= 0)
-          tma_load3(kv_smem + stage * C::kTile + half * C::kHalf + (chunk << args.chunk_shift) * 128, map, half * 64,
-                    k0 & (a.v.page - 1) & ~(args.chunk - 1), page * s.heads + g.head, &bars.full[stage]);
-        ++at;
-        return true;
-      };
-      int now = page_of(0), next = page_of(1), later;
-      if (g.dual) {
-        for (int j = 0; ok && j < n; ++j) {
-          later = page_of(j + 2);
-          ok = load(&args.maps.k, j, now) && load(&args.maps.v, j, now);
-          now = next;
-          next = later;
-        }
-      } else {
-        ok = load(&args.maps.k, 0, now);
-        for (int j = 0; ok && j < n; ++j) {
-          later = page_of(j + 2);
-          if (j + 1 < n) ok = load(&args.maps.k, j + 1, next);
-          ok = ok && load(&args.maps.v, j, now);
-          now = next;
-          next = later;
-        }
-      }
-    }
-    if (!ok) {  // leave no load in flight
-      for (uint32_t i = at > C::kStages ? at - C::kStages : 0; i < at; ++i)
-        mbar_wait_bounded(&bars.full[i % C::kStages], (i / C::kStages) & 1, a.v.err, kDevErrTimeout, bound);
-      for (uint32_t i = qc > 2 ? qc - 2 : 0; i < qc; ++i)
-        mbar_wait_bounded(&bars.q_full[i & 1], (i >> 1) & 1, a.v.err, kDevErrTimeout, bound);
-    }
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ MMAs
-    constexpr uint32_t qk = mma_desc(128, 128, false), pv = mma_desc(128, D, true);
-    uint32_t at = 0, qc = 0, np[2] = {0, 0}, no[2] = {0, 0};
-    bool ok = true;
-    auto stage_wait = [&](uint32_t p) { return wait(&bars.full[p % C::kStages], (p / C::kStages) & 1, a.wait_cycles); };
-    while (ok && walk.next(a, cta, &g)) {
-      const int n = g.t1 - g.t0;
-      const int count[2] = {g.dual ? n : (n + 1) / 2, g.dual ? n : n / 2};
-      const int tiles_q = g.dual ? 2 : 1;
-      for (int i = 0; ok && i < tiles_q; ++i)
-        ok = wait(&bars.q_full[(qc + i) & 1], ((qc + i) >> 1) & 1, a.wait_cycles);
-      auto scores = [&](int st, int i) {
-        const uint32_t p = at + k_at(g.dual, g.dual ? i : 2 * i + st);
-        if (!stage_wait(p)) return false;
-        if (lane == 0) {
-          const uint32_t q = q_smem + ((qc + (g.dual ? st : 0)) & 1) * C::kTile;
-          const uint32_t k = kv_smem + p % C::kStages * C::kTile;
-#pragma unroll
-          for (int x = 0; x < D / 16; ++x) {
-            const uint32_t off = x / 4 * C::kHalf + x % 4 * 32;
-            mma_ss(tmem + st * 128, smem_desc(q + off, 16, 1024), smem_desc(k + off, 16, 1024), qk, x > 0);
-          }
-          mma_commit(&bars.s_full[st]);
-          if (!g.dual || st == 1) mma_commit(&bars.empty[p % C::kStages]);
-        }
-        __syncwarp();
-        return true;
-      };
-      for (int st = 0; st < 2; ++st)
-        if (ok && count[st]) ok = scores(st, 0);
-      for (int i = 0; ok && i < count[0]; ++i) {
-        for (int st = 0; ok && st < 2; ++st) {
-          if (i >= count[st]) continue;
-          const uint32_t p = at + v_at(g.dual, g.dual ? i : 2 * i + st, n);
-          ok = wait(&bars.p_ready[st], np[st]++ & 1, bound) && stage_wait(p);
-          if (ok && i == 0) ok = wait(&bars.o_free[st], (no[st]++ & 1) ^ 1, bound);
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t v = kv_smem + p % C::kStages * C::kTile;
-#pragma unroll
-            for (int x = 0; x < kKeys / 16; ++x) {
-              const uint64_t desc = smem_desc(v + x * 2048, C::kHalf, 1024);
-              mma_ts(tmem + 256 + st * D, tmem + st * 128 + x * 8, desc, pv, i > 0 || x > 0);
-              if (WIDE) mma_ts(tmem + 256 + st * D, tmem + st * 128 + 64 + x * 8, desc, pv, true);
-            }
-            if (!g.dual || st == 1) mma_commit(&bars.empty[p % C::kStages]);
-            if (i + 1 == count[st]) mma_commit(&bars.o_full[st]);
-          }
-          __syncwarp();
-          if (i + 1 < count[st]) ok = scores(st, i + 1);
-        }
-      }
-      if (ok && lane == 0)
-        for (int i = 0; i < tiles_q; ++i) mma_commit(&bars.q_empty[(qc + i) & 1]);
-      __syncwarp();
-      at += 2 * n;
-      qc += tiles_q;
-    }
-    if (!ok) {  // leave no MMA in flight
-      if (lane == 0) mma_commit(&bars.drain);
-      __syncwarp();
-      mbar_wait_bounded(&bars.drain, 0, a.v.err, kDevErrTimeout, bound);
-    }
+  if (warp < 8) {
+    more_registers<kStreamRegs>();
+    Stream<D, WIDE> s(args, bars, wait, base + 2 * C::kTile, tmem);
+    s.run(walk, cta);
   } else {
-    // ------------------------------------------------------------ weights
-    const int st = warp >> 2;
-    const int r = (warp & 3) * 32 + lane;  // this thread's row of the tile
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const uint32_t ts = tmem + lanes + st * 128, to = tmem + lanes + 256 + st * D;
-    const float c = a.scale_log2;
-    uint32_t at = 0, ns = 0, no = 0;
-    bool ok = true;
-    while (ok && walk.next(a, cta, &g)) {
-      const int n = g.t1 - g.t0;
-      const int count = g.dual ? n : (n + 1 - st) / 2;
-      const uint32_t first_at = at;
-      at += 2 * n;
-      if (count == 0) continue;
-      int b, rem;
-      bool valid;
-      if (g.own) {
-        b = g.b;
-        rem = g.tile * s.own_tile + r;
-        valid = rem < s.rows;
-      } else {
-        const int rt = g.dual ? 2 * g.tile + st : g.tile + s.duals;
-        if (s.seqs_per_tile) {
-          const int x = r / s.rows;
-          b = rt * s.seqs_per_tile + x;
-          rem = r - x * s.rows;
-          valid = x < s.seqs_per_tile && b < s.batch;
-        } else {
-          b = rt / s.tiles_per_seq;
-          rem = (rt - b * s.tiles_per_seq) * s.prefix_tile + r;
-          valid = rem < s.rows;
-        }
+    fewer_registers<kOtherRegs>();
+    if (warp == 8) {
+      Loader<D> x(args, bars, wait, q_smem, kv_smem);
+      if (!x.run(walk, cta)) {  // leave no load in flight
+        for (uint32_t i = x.at.index > C::kStages ? x.at.index - C::kStages : 0; i < x.at.index; ++i)
+          mbar_wait_bounded(&bars.full[i % C::kStages], (i / C::kStages) & 1, a.v.err, kDevErrTimeout, kCopyWaitCycles);
+        for (uint32_t i = x.qc > 2 ? x.qc - 2 : 0; i < x.qc; ++i)
+          mbar_wait_bounded(&bars.q_full[i & 1], (i >> 1) & 1, a.v.err, kDevErrTimeout, kCopyWaitCycles);
       }
-      int slot, row_end = 0;
-      const int first = g.own ? s.prefix : 0;
-      int end = s.prefix;
-      if (g.own) end = prefix_len(a, g.b, &slot);
-      if (valid) row_end = min(end, tokens_seen(s, prefix_len(a, b, &slot), rem % s.nq));
-      const bool work = __any_sync(0xffffffffu, valid);
-      float m = -INFINITY, l = 0.f;
-      for (int i = 0; ok && i < count; ++i) {
-        const int j = g.dual ? i : 2 * i + st;
-        const int k0 = first + (g.t0 + j) * kKeys;
-        ok = wait(&bars.s_full[st], ns++ & 1, bound);
-        if (!ok) break;
-        tc_fence_after();
-        if (end - k0 < kKeys) {  // rows of V behind the sequence
-          const uint32_t p = first_at + v_at(g.dual, j, n);
-          ok = wait(&bars.full[p % C::kStages], (p / C::kStages) & 1, bound);
-          if (!ok) break;
-          if (r >= end - k0) {
-            char* v = base + (2 + p % C::kStages) * C::kTile + r * 128;
-#pragma unroll
-            for (int x = 0; x < D / 64; ++x)
-#pragma unroll
-              for (int y = 0; y < 8; ++y) *reinterpret_cast<uint4*>(v + x * C::kHalf + y * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-        }
-        if (work) {
-          uint32_t x[kKeys];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(x + 32 * q, ts + 32 * q);
-          tmem_wait_ld();
-          float* f = reinterpret_cast<float*>(x);
-          if (args.flip) {
-#pragma unroll
-            for (int k = 0; k < kKeys; ++k) f[k] = -f[k];
-          }
-          const int lim = row_end - k0;
-          if (__any_sync(0xffffffffu, lim < kKeys)) {
-#pragma unroll
-            for (int k = 0; k < kKeys; ++k) f[k] = k < lim ? f[k] : -INFINITY;
-          }
-          float t0 = f[0], t1 = f[1], t2 = f[2], t3 = f[3];
-#pragma unroll
-          for (int k = 4; k < kKeys; k += 4) {
-            t0 = fmaxf(t0, f[k]);
-            t1 = fmaxf(t1, f[k + 1]);
-            t2 = fmaxf(t2, f[k + 2]);
-            t3 = fmaxf(t3, f[k + 3]);
-          }
-          const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * c;
-          float fix = 1.f;
-          if (m == -INFINITY) {
-            m = top;  // nothing of this row in O yet
-          } else if (top > m + kSlack) {
-            fix = exp2_approx(m - top);
-            m = top;
-          }
-          if (i > 0 && __any_sync(0xffffffffu, fix != 1.f)) {
-            l *= fix;
-#pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-              uint32_t y[32];
-              tmem_ld32(y, to + 32 * q);
-              tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * fix);
-              tmem_st32(to + 32 * q, y);
-            }
-          }
-          const float off = m == -INFINITY ? 0.f : -m;
-          float u0 = 0.f, u1 = 0.f;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t hi[16], lo[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float p0 = exp2_approx(fmaf(f[32 * q + 2 * k], c, off));
-              const float p1 = exp2_approx(fmaf(f[32 * q + 2 * k + 1], c, off));
-              u0 += p0;
-              u1 += p1;
-              hi[k] = pack_bf16(p0, p1);
-              if (WIDE)
-                lo[k] = pack_bf16(p0 - __uint_as_float(hi[k] << 16), p1 - __uint_as_float(hi[k] & 0xffff0000u));
-            }
-            tmem_st16(ts + 16 * q, hi);
-            if (WIDE) tmem_st16(ts + 64 + 16 * q, lo);
-          }
-          l += u0 + u1;
-          tmem_wait_st();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.p_ready[st]);
-      }
-      if (!ok) break;
-      ok = wait(&bars.o_full[st], no++ & 1, bound);
-      if (!ok) break;
-      tc_fence_after();
-      if (work) {
-        const size_t out = (size_t)g.slot + (g.own ? st * (s.own_slot_rows / 2) : st * s.prefix_tile) + r;
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-          uint32_t y[32];
-          tmem_ld32(y, to + 32 * q);
-          tmem_wait_ld();
-          if (valid) {
-#pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<uint4*>(a.acc + out * D + 32 * q + k) = make_uint4(y[k], y[k + 1], y[k + 2], y[k + 3]);
-          }
-        }
-        if (valid) a.ml[out] = make_float2(m, l);
-      }
-      tc_fence_before();
+    } else if (warp == 9) {
+      Issuer<D, WIDE> x(args, bars, wait, q_smem, kv_smem, tmem);
+      x.run(walk.pos < walk.hi && walk.pos < a.s.dual_total);
+      // leave no MMA in flight, whatever ended the run
+      if (elect_one()) mma_commit(&bars.drain);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.o_free[st]);
+      mbar_wait_bounded(&bars.drain, 0, a.v.err, kDevErrTimeout, kCopyWaitCycles);
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_free(tmem, kTmemCols);
+  if (warp == 10) tmem_free(tmem, kTmemCols);
 }
 
 // ---------------------------------------------------------------- host
@@ -483,7 +700,8 @@ cudaError_t launch_prefix_tc(const zha_pages* p, const PrefixArgs& a, int head_d
   const cuuint64_t q[4] = {d, (cuuint64_t)s.rows, (cuuint64_t)s.heads, (cuuint64_t)s.batch};
   const cuuint32_t rows = s.rows < kRows ? s.rows : kRows;
   const cuuint32_t own[4] = {64, rows, 1, 1};
-  const cuuint32_t shared[4] = {64, rows, 1, (cuuint32_t)(s.seqs_per_tile ? s.seqs_per_tile : 1)};
+  const int together = s.prefix_parts == 4 ? s.batch : s.seqs_per_tile ? s.seqs_per_tile : 1;
+  const cuuint32_t shared[4] = {64, rows, 1, (cuuint32_t)together};
   x.chunk = p->desc.page_tokens < kKeys ? p->desc.page_tokens : kKeys;
   x.chunk_shift = 0;
   while ((1 << x.chunk_shift) < x.chunk) ++x.chunk_shift;

@@ -28,12 +28,24 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// 128-byte-swizzled operand in shared memory.  K-major: rows of 128 bytes (64 elements along
-// K) in groups of 8 (sbo = 1,024 bytes apart); lbo unused.  MN-major: 64 elements along MN by 8 along K
-// make a group; lbo is the stride to the next 64 along MN, sbo to the next 8 along K.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) |
-         (1ull << 46) | (2ull << 61);
+// One lane of the warp; the compiler knows that the branch it guards is taken by one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// Lane 0's x: a value that all lanes hold anyway, in a form that can live in a uniform register, which
+// is what MMA operands are read from.
+template <typename T>
+__device__ __forceinline__ T same(T x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// 128-byte-swizzled operand in shared memory at 16 times addr16.  K-major: rows of 128 bytes (64 elements along
+// K) in groups of 8, 1,024 bytes apart; lbo unused.  MN-major: 64 elements along MN by 8 along K
+// make a group; lbo is the stride to the next 64 along MN, 1,024 that to the next 8 along K.
+__device__ __forceinline__ uint64_t desc_of(uint32_t addr16, uint32_t lbo) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(addr16 | (lbo >> 4) << 16), "r"((1024u >> 4) | (1u << 14) | (2u << 29)));
+  return d;
 }
 // bf16 x bf16 -> fp32, M x N; b_mn: B is MN-major.
 __host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool b_mn) {
@@ -67,12 +79,11 @@ __device__ __forceinline__ void tmem_ld32(uint32_t* r, uint32_t addr) {
       : ZHA_R8(r, 0), ZHA_R8(r, 8), ZHA_R8(r, 16), ZHA_R8(r, 24)
       : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+__device__ __forceinline__ void tmem_ld16(uint32_t* r, uint32_t addr) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
-      ZHA_W8(r, 0), ZHA_W8(r, 8), ZHA_W8(r, 16), ZHA_W8(r, 24)
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : ZHA_R8(r, 0), ZHA_R8(r, 8)
+      : "r"(addr));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
@@ -84,6 +95,9 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
 #undef ZHA_R8
 #undef ZHA_W8
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 // Tiled loads (x times the element size is a multiple of 16 bytes at every call).
 __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
@@ -103,6 +117,51 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+constexpr float kExp2C0 = 0.999924541f, kExp2C1 = 0.693136752f, kExp2C2 = 0.242639482f, kExp2C3 = 0.0558382832f;
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(uint64_t x, float* lo, float* hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t neg2(uint64_t a) { return a ^ 0x8000000080000000ull; }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// 2^x of two floats on the FMA pipes, for x <= 8 or so: x is split into the nearest integer n, read off the low
+// bits of x + 1.5 * 2^23, and the rest f in [-1/2, 1/2]; 2^f is a cubic through Chebyshev nodes of
+// that interval, off by less than 1.1e-4 of itself; n is added to the exponent.  x below -126 gives
+// 2^-126, which no sum of weights sees.
+__device__ __forceinline__ void exp2_by_fma(uint64_t x, float* lo, float* hi) {
+  float a, b;
+  split(x, &a, &b);
+  x = pair(fmaxf(a, -126.f), fmaxf(b, -126.f));
+  const uint64_t n = add2(x, pair(12582912.f, 12582912.f));
+  const uint64_t f = add2(x, neg2(add2(n, pair(-12582912.f, -12582912.f))));
+  uint64_t p = fma2(f, pair(kExp2C3, kExp2C3), pair(kExp2C2, kExp2C2));
+  p = fma2(f, p, pair(kExp2C1, kExp2C1));
+  p = fma2(f, p, pair(kExp2C0, kExp2C0));
+  float na, nb, pa, pb;
+  split(n, &na, &nb);
+  split(p, &pa, &pb);
+  *lo = __uint_as_float(__float_as_uint(pa) + (__float_as_uint(na) << 23));
+  *hi = __uint_as_float(__float_as_uint(pb) + (__float_as_uint(nb) << 23));
 }
 // Two floats to bf16 (nearest even): lo in the low half.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
