@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   const int n = own_key_tiles(s, len);
   if (n > 0) {
     const int x = head * s.own_tiles + rem / s.own_tile;
-    item(s.prefix_total + a.cum[b] * group + x * n, n, s.streams, s.own_parts,
+    item(s.prefix_total + a.cum[b] * group + x * (n + kOwnStart) + kOwnStart, n, s.streams, s.own_parts,
          s.own_slot0 + ((long long)b * group + x) * s.own_slot_rows + rem % s.own_tile, s.own_slot_rows,
          s.own_slot_rows / (s.streams * s.own_parts));
   }
@@ -403,7 +403,7 @@ bool plan(const zha_pages* p, int batch, int q_heads, int nq, long long prefix, 
   // all key tiles, sequences as long as they may be, are counted in 31 bits
   const long long most = (long long)p->desc.max_seq_pages * p->desc.page_tokens;
   if ((long long)heads * row_tiles * s->prefix_keys +
-          (long long)batch * heads * s->own_tiles * ceil_div(most, s->tile_keys) > 0x7fffffffLL)
+          (long long)batch * heads * s->own_tiles * (ceil_div(most, s->tile_keys) + kOwnStart) > 0x7fffffffLL)
     return false;
   s->dual_total = heads * s->duals * s->prefix_keys;
   s->prefix_total = s->dual_total + heads * s->singles * s->prefix_keys;

@@ -7,8 +7,8 @@
 //   single  one row tile against the shared tokens
 //   own     one sequence's rows (or a slice) against its tokens behind the prefix
 // All items' key tiles, laid end to end in that order, are cut into one equal share per CTA, so that
-// no CTA waits for a long sequence (the kinds' tiles cost about the same: their 64 KB of keys
-// and values).  A CTA's part of an item is a segment; its
+// no CTA waits for a long sequence.  The kinds' tiles cost about the same, their 64 KB of keys and values;
+// an own item counts for one tile more, for its start and end.  A CTA's part of an item is a segment; its
 // result (maximum, sum and weighted values, fp32) goes to the slot item + cta, which is unique
 // because both only grow along the order.  A second kernel joins a row's slots.
 //
@@ -50,7 +50,7 @@ struct PrefixArgs {
   const void* K;
   const void* V;
   const int* seqs;
-  int* cum;        // [batch + 1] own key tiles before a sequence (written by CTA 0 for the join)
+  int* cum;        // [batch + 1] own cost before a sequence, per row tile (written by CTA 0 for the join)
   float2* ml;      // [slot rows] maximum (base 2, scaled) and sum
   float* acc;      // [slot rows, head_dim]
   void* O;
@@ -81,6 +81,8 @@ __device__ __forceinline__ int share_start(int c, int T, int ctas) {
   return c * each + min(c, more);
 }
 
+constexpr int kOwnStart = 1;  // what an own item costs besides its tiles
+
 enum SegmentKind { kDual = 0, kSingle = 1, kOwn = 2 };
 
 struct Segment {
@@ -100,7 +102,7 @@ struct Walk {
   int b, n;             // own part: the sequence at pos and its key tiles
   int len, pages;       // its tokens and slot
   int next_len, next_pages;  // those of sequence b + 1, fetched ahead
-  int item, t;          // its row tile (heads * own_tiles of them) and the key tile at pos
+  int item, t;          // its row tile (heads * own_tiles of them), and its key tile at pos; below 0: in its start
 
   __device__ __forceinline__ void fetch(const PrefixArgs& a) {
     next_len = 0;
@@ -128,7 +130,7 @@ struct Walk {
     }
     const int group = s.heads * s.own_tiles;
     if (t == n) {  // the next item
-      t = 0;
+      t = -kOwnStart;
       if (++item == group) {
         item = 0;
         do {
@@ -140,6 +142,11 @@ struct Walk {
         } while (n == 0 && b < s.batch);
         if (b >= s.batch) return false;
       }
+    }
+    if (t < 0) {
+      pos -= t;
+      t = 0;
+      if (pos >= hi) return false;
     }
     g->t0 = t;
     g->t1 = min(n, t + hi - pos);
@@ -156,19 +163,24 @@ struct Walk {
   }
 };
 
+__device__ __forceinline__ int own_cost(const PrefixShape& s, int len) {
+  const int n = own_key_tiles(s, len);
+  return n ? n + kOwnStart : 0;
+}
+
 // Finds CTA `cta`'s share; all of the CTA's `threads` threads call it.  sm: at least
 // threads / 32 + 4 ints.  CTA 0 also leaves the sums for the join and checks the call's slots.
 __device__ __forceinline__ Walk find_share(const PrefixArgs& a, int cta, int threads, int* sm) {
   const PrefixShape& s = a.s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = threads / 32;
   const int group = s.heads * s.own_tiles;
-  int* out = sm + warps;  // sequence, key tiles before it, its tokens and slot
+  int* out = sm + warps;  // sequence, cost before it, its tokens and slot
   // the total first: a share's borders depend on it
   int total = 0, mine = 0, len_first = 0, slot_first = 0;
   for (int b = tid; b < s.batch; b += threads) {
     int slot;
     const int len = prefix_len(a, b, &slot);
-    mine += own_key_tiles(s, len);
+    mine += own_cost(s, len);
     if (b == tid) {
       len_first = len;
       slot_first = slot;
@@ -197,7 +209,7 @@ __device__ __forceinline__ Walk find_share(const PrefixArgs& a, int cta, int thr
       const int b = b0 + tid;
       int slot = slot_first, len = len_first;
       if (b0 > 0) len = b < s.batch ? prefix_len(a, b, &slot) : 0;
-      const int n = own_key_tiles(s, len);
+      const int n = own_cost(s, len);
       int v = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -228,9 +240,9 @@ __device__ __forceinline__ Walk find_share(const PrefixArgs& a, int cta, int thr
       w.len = out[2];
       w.pages = out[3];
       w.n = own_key_tiles(s, w.len);
-      const int y = x - out[1] * group;
-      w.item = y / w.n;
-      w.t = y - w.item * w.n;
+      const int y = x - out[1] * group, cost = w.n + kOwnStart;
+      w.item = y / cost;
+      w.t = y - w.item * cost - kOwnStart;
       w.fetch(a);
     }
     __syncthreads();

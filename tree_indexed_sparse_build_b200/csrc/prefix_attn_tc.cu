@@ -9,10 +9,11 @@
 // join adds what the two streams leave of a segment.
 //
 //   warps 0-3, 4-7  stream 0, 1: maximum, exp2, sum, P; correction and output of O
-//   warp 8          TMA: queries, and keys and values page by page into a ring
-//   warp 9          MMA issue (one lane), for both streams: an issuer each let the streams fall into
-//                   step, so that MMAs and weights took turns instead of overlapping
-//   warp 10         TMEM; warps 10 and 11 give their registers to the streams' warps
+//   warp 8, 9       TMA: queries and keys, values, page by page into a ring each.  A load for every (page,
+//                   64 columns) takes the issuing warp about 100 clocks, so one warp for both was too slow
+//   warp 10, 11     MMA issue (one lane) for stream 0, 1; warp 10 also holds TMEM.  Looking for the next
+//                   operands takes an issuer 500 clocks, in which the other issues.  They take turns: left
+//                   alone the streams fall into step, and MMAs and weights alternate instead of overlapping
 //
 // Up to 32 rows fill one warp's lanes.  Then the queries are loaded four times, into the lanes of each
 // warp, and each weighs a quarter of the keys (P is zero elsewhere): a fourth of the
@@ -56,26 +57,29 @@ template <int D>
 struct Tc {
   static constexpr int kTile = 128 * D * 2;  // bytes of 128 rows
   static constexpr int kHalf = 128 * 128;    // bytes of 128 rows x 64 elements
-  static constexpr int kStages = D == 128 ? 5 : 10;
-  static constexpr size_t kSmem = 1024 + (size_t)(2 + kStages) * kTile + 1024;
+  static constexpr int kKStages = D == 128 ? 3 : 5, kVStages = D == 128 ? 2 : 5;
+  static constexpr size_t kSmem = 1024 + (size_t)(2 + kKStages + kVStages) * kTile + 1024;
 };
 
 struct Bars {
-  uint64_t full[10], empty[10], q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2], o_free[2], drain;
-  int2 meta[10];  // of a ring place: its keys, and PlaceFlags
+  uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2], o_free[2], turn[2], drain[2];
+  int2 k_meta[5], v_meta[5];  // of a ring place: its keys, and TileFlags
   uint32_t tmem;
   int gone;  // a wait ran out
   int share[kThreads / 32 + 4];
 };
 static_assert(sizeof(Bars) <= 1024, "the barriers' page");
 
-// What the issuer has to know of a ring place, written by the loader.
-enum PlaceFlags {
-  kFirst = 1,     // keys: the segment's first tile; values: its stream's first of the segment
-  kLast = 2,      // .. last
-  kPaired = 4,    // a dual tile: both streams use the place
-  kLoneNext = 8,  // a dual tile that no dual tile follows
-  kEnd = 16       // no tile: the share is done
+// What the issuers have to know of a tile, written by the loaders.
+enum TileFlags {
+  kFirst = 1,   // its stream's first tile of the segment
+  kLast = 2,    // .. last
+  kPaired = 4,  // a dual tile: both streams'
+  kAlone = 8,   // keys: one stream alone uses the queries
+  kLoneNext = 16,  // a dual tile that no dual tile follows
+  kEnd = 32,    // no tile: the stream is done
+  kQuery = 64   // keys, from here up: which query tile (mod 4)
 };
 
 // Bounded waits on the barriers of one CTA.  A whole warp waits, and all of its lanes get the same answer:
@@ -122,13 +126,12 @@ struct Tiles {
   }
 };
 
-// A place in the ring and how often the ring has gone round.
+// A place in a ring and how often the ring has gone round.  Place y holds tile y.
 template <int STAGES>
 struct Place {
   int stage = 0;
-  uint32_t round = 0, index = 0;
-  __device__ __forceinline__ void add(int n) {  // n <= STAGES
-    index += n;
+  uint32_t round = 0;
+  __device__ __forceinline__ void add(int n) {  // n <= 2
     stage += n;
     if (stage >= STAGES) {
       stage -= STAGES;
@@ -145,7 +148,7 @@ __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec
 // The kernel launches with 168 registers a thread: 384 x 168 = 128 x (2 x 192 + 120).
 constexpr int kStreamRegs = 192, kOtherRegs = 120;
 
-// ---- warp 8
+// ---- warps 8 and 9
 
 template <int D>
 struct Loader {
@@ -154,14 +157,13 @@ struct Loader {
   const PrefixArgs& a;
   Bars& bars;
   const Waiter& wait;
-  uint32_t q_smem, kv_smem;
+  uint32_t q_smem, ring;  // shared addresses of the queries and of this loader's ring
   int lane, per_tile, chunk, half;
   bool mine;
-  Place<C::kStages> at;
-  uint32_t qc = 0;  // query tiles loaded
+  uint32_t qc = 0, tiles = 0;  // query tiles and key tiles loaded
 
   __device__ __forceinline__ Loader(const TcArgs& x, Bars& b, const Waiter& w, uint32_t q, uint32_t kv)
-      : args(x), a(x.a), bars(b), wait(w), q_smem(q), kv_smem(kv), lane(threadIdx.x & 31) {
+      : args(x), a(x.a), bars(b), wait(w), q_smem(q), ring(kv), lane(threadIdx.x & 31) {
     per_tile = kKeys >> args.chunk_shift;
     chunk = lane % per_tile;
     half = lane / per_tile;
@@ -203,64 +205,74 @@ struct Loader {
     return a.v.num_pages;
   }
 
-  // Order of the ring: K0 V0 K1 V1 .. for dual tiles, which both streams read together, then
-  // K0 K1 V0 K2 V1 .., tile x for stream x & 1; where the next K would be, a place that says that there is none.
+  // The share's key tiles, KEYS: with the queries, else the values.
+  template <bool KEYS>
   __device__ __forceinline__ bool run(const Walk& walk, int cta) {
+    constexpr int kStages = KEYS ? C::kKStages : C::kVStages;
+    uint64_t* const full = KEYS ? bars.k_full : bars.v_full;
+    uint64_t* const empty = KEYS ? bars.k_empty : bars.v_empty;
+    int2* const meta = KEYS ? bars.k_meta : bars.v_meta;
+    const CUtensorMap* const map = KEYS ? &args.maps.k : &args.maps.v;
+    Place<kStages> at;
     Tiles x(a, walk, cta);
     int page = x.any ? page_of(x) : -1;
-    struct Place1 {
-      int head, k0, n, page, flags;
-    } now, before;
-    before = now = {0, 0, 0, -1, 0};
-    bool pending = false;  // the tile before still lacks its values
-    bool ended = false;
-    while (!ended) {
-      const bool any = x.any, dual = any && x.dual();
-      int k_flags = kEnd;
-      if (any) {
-        const int by = dual ? 1 : 2;
-        if (x.t == x.g.t0)
-          for (int i = 0; i < 1 + dual; ++i)
-            if (!queries(x.g, x.g.tile + i)) return false;
-        k_flags = (x.t == x.g.t0 ? kFirst : 0) | (x.t + 1 == x.g.t1 ? kLast : 0) | (dual ? kPaired : 0);
-        now = {x.g.head, x.k0(a), x.keys(a), page, dual ? kPaired : 0};
-        if (x.t < x.g.t0 + by) now.flags |= kFirst;
-        if (x.t + by >= x.g.t1) now.flags |= kLast;
-        x.step(a, cta);
-        if (x.any) page = page_of(x);
-        if (dual && !(x.any && x.dual())) now.flags |= kLoneNext;
-      } else {
-        ended = true;
+    while (x.any) {
+      const bool dual = x.dual();
+      const int by = dual ? 1 : 2;
+      if (KEYS && x.t == x.g.t0)
+        for (int i = 0; i < 1 + dual; ++i)
+          if (!queries(x.g, x.g.tile + i)) return false;
+      int flags = dual ? kPaired : 0;
+      if (x.t < x.g.t0 + by) flags |= kFirst;
+      if (x.t + by >= x.g.t1) flags |= kLast;
+      if (KEYS) {
+        if (dual || x.g.t1 - x.g.t0 == 1) flags |= kAlone;
+        flags |= ((qc - 1 - dual) & 3) * kQuery;
       }
-#pragma unroll 1
-      for (int values = 0; values < 2; ++values) {
-        if (values && !dual && !pending) break;
-        const bool here = !values || dual;  // this tile, or the one before
-        const int n = here ? now.n : before.n, k0 = here ? now.k0 : before.k0, head = here ? now.head : before.head;
-        const int id = here ? now.page : before.page, chunks = (n + args.chunk - 1) >> args.chunk_shift;
-        if (!wait(&bars.empty[at.stage], at.round ^ 1)) return false;
+      const int n = x.keys(a), y = x.k0(a) & (a.v.page - 1) & ~(args.chunk - 1), z = page * a.s.heads + x.g.head;
+      const bool load = page >= 0;
+      x.step(a, cta);
+      if (x.any) page = page_of(x);
+      if (dual && !(x.any && x.dual())) flags |= kLoneNext;
+      if (!wait(&empty[at.stage], at.round ^ 1)) return false;
+      if (lane == 0) {
+        meta[at.stage] = make_int2(n, flags);
+        mbar_arrive_expect_tx(&full[at.stage], ((n + args.chunk - 1) >> args.chunk_shift) * args.chunk * D * 2);
+      }
+      __syncwarp();
+      if (load)
+        tma_load3(ring + at.stage * C::kTile + half * C::kHalf + (chunk << args.chunk_shift) * 128, map, half * 64, y, z,
+                  &full[at.stage]);
+      at.add(1);
+      ++tiles;
+    }
+    if (KEYS)
+      for (int i = 0; i < 2; ++i) {  // where each stream's next tile would be
+        if (!wait(&empty[at.stage], at.round ^ 1)) return false;
         if (lane == 0) {
-          bars.meta[at.stage] = make_int2(n, values ? (here ? now.flags : before.flags) : k_flags);
-          if (values || any)
-            mbar_arrive_expect_tx(&bars.full[at.stage], chunks * args.chunk * D * 2);
-          else
-            mbar_arrive(&bars.full[at.stage]);
+          meta[at.stage] = make_int2(0, kEnd);
+          mbar_arrive(&full[at.stage]);
         }
         __syncwarp();
-        if (id >= 0 && (values || any))
-          tma_load3(kv_smem + at.stage * C::kTile + half * C::kHalf + (chunk << args.chunk_shift) * 128,
-                    values ? &args.maps.v : &args.maps.k, half * 64, k0 & (a.v.page - 1) & ~(args.chunk - 1),
-                    id * a.s.heads + head, &bars.full[at.stage]);
         at.add(1);
+        ++tiles;
       }
-      pending = any && !dual;
-      before = now;
-    }
     return true;
+  }
+
+  // After a wait that ran out: leaves no load in flight.
+  template <bool KEYS>
+  __device__ __forceinline__ void drain() {
+    constexpr uint32_t stages = KEYS ? C::kKStages : C::kVStages;
+    uint64_t* const full = KEYS ? bars.k_full : bars.v_full;
+    for (uint32_t i = tiles > stages ? tiles - stages : 0; i < tiles; ++i)
+      mbar_wait_bounded(&full[i % stages], (i / stages) & 1, a.v.err, kDevErrTimeout, kCopyWaitCycles);
+    for (uint32_t i = qc > 2 ? qc - 2 : 0; i < qc; ++i)
+      mbar_wait_bounded(&bars.q_full[i & 1], (i >> 1) & 1, a.v.err, kDevErrTimeout, kCopyWaitCycles);
   }
 };
 
-// ---- warp 9
+// ---- warps 10 and 11
 
 template <int D, bool WIDE>
 struct Issuer {
@@ -268,99 +280,93 @@ struct Issuer {
   const PrefixArgs& a;
   Bars& bars;
   const Waiter& wait;
-  uint32_t q_smem, kv_smem, tmem;
+  uint32_t q_smem, k_smem, v_smem, tmem;
+  int st;
 
-  __device__ __forceinline__ Issuer(const TcArgs& x, Bars& b, const Waiter& w, uint32_t q, uint32_t kv, uint32_t t)
-      : a(x.a), bars(b), wait(w), q_smem(q), kv_smem(kv), tmem(t) {}
+  __device__ __forceinline__ Issuer(const TcArgs& x, Bars& b, const Waiter& w, uint32_t q, uint32_t t, int stream)
+      : a(x.a), bars(b), wait(w), q_smem(q), k_smem(q + 2 * C::kTile), v_smem(k_smem + C::kKStages * C::kTile), tmem(t), st(stream) {}
 
-  // One lane: S = queries in buffer `buf` times the keys in `stage`; then the barriers that wait for it.
-  __device__ __forceinline__ void scores(int st, int buf, int stage, int2 m) {
-    const uint32_t desc = same(mma_desc(128, (m.x + 15) & ~15, false)), d = same(tmem + st * 128);
-    const uint32_t q = same((q_smem + buf * C::kTile) >> 4), k = same((kv_smem + stage * C::kTile) >> 4);
-    if (elect_one()) {
-#pragma unroll
-      for (int x = 0; x < D / 16; ++x) {
-        const uint32_t off = (x / 4 * C::kHalf + x % 4 * 32) >> 4;
-        mma_ss(d, desc_of(q + off, 16), desc_of(k + off, 16), desc, x > 0);
-      }
-      mma_commit(&bars.s_full[st]);
-      if (!(m.y & kPaired) || st == 1) mma_commit(&bars.empty[stage]);
-      if (m.y & kLast) mma_commit(&bars.q_empty[buf]);
-    }
-    __syncwarp();
-  }
-
-  // One lane: O (+)= P times the values in `stage`; then the barriers that wait for it.
-  __device__ __forceinline__ void values(int st, int stage, int2 m) {
-    constexpr uint32_t desc = mma_desc(128, D, true);
-    const uint32_t v = same((kv_smem + stage * C::kTile) >> 4), o = same(tmem + 256 + st * D), w = same(tmem + st * 128);
-    const int steps = same((m.x + 15) / 16);
-    const bool add = same(!(m.y & kFirst));
-    if (elect_one()) {
-#pragma unroll
-      for (int x = 0; x < kKeys / 16; ++x) {
-        if (x >= steps) break;
-        mma_ts(o, w + x * 8, desc_of(v + x * 128, C::kHalf), desc, add || x > 0);
-        if (WIDE) mma_ts(o, w + 64 + x * 8, desc_of(v + x * 128, C::kHalf), desc, true);
-      }
-      if (!(m.y & kPaired) || st == 1) mma_commit(&bars.empty[stage]);
-      if (m.y & kLast) mma_commit(&bars.o_full[st]);
-    }
-    __syncwarp();
-  }
-
-  // The place of a stream's next keys, or of none.
-  __device__ __forceinline__ bool look(const Place<C::kStages>& kp, uint32_t qc, int st, int2* k) {
-    *k = bars.meta[kp.stage];
-    const uint32_t q = qc + (k->y & kPaired ? st : 0);
-    return !(k->y & kFirst) || wait(&bars.q_full[q & 1], (q >> 1) & 1, a.wait_cycles);
-  }
-
-  // pairs: the share starts with a dual tile.
+  // This stream's tiles: S of the first, then again and again O += P V of one and S of the next.  A tile's keys are
+  // released by two arrivals, its queries too: one of each stream, or two of the only one that uses them.
+  //
+  // An issuer waits for a ring place whose stage held, three (keys; values: two, the stream's own) tiles
+  // before, a tile of the other stream.  A parity says that a phase is over only to somebody who knows that
+  // the phase before is.  Here the turns say so: the other stream issued its scores of that tile before it gave
+  // up the turn that this stream used last.
   __device__ __forceinline__ bool run(bool pairs) {
-    Place<C::kStages> kp, vp;  // ring places of the next scores and values
-    vp.add(pairs ? 1 : 2);
-    uint32_t qc = 0, phase = 0;  // query tiles used up; bits 0, 1: phases of p_ready, 2, 3: of o_free
-    int todo = 0;                // tiles whose scores are issued and whose values are not
-    bool more = true, lone = false;
-    int st = 0;
-    for (int ahead = 2; more || todo; ahead -= ahead > 0, st ^= 1) {  // scores run two tiles ahead of values
-      int2 k;
-      bool seen = false;
-      if (ahead == 0) {
-        const int stage = vp.stage;
-        if (!wait(&bars.full[stage], vp.round, a.wait_cycles)) return false;
-        const int2 v = bars.meta[stage];
-        if ((v.y & kFirst) && !wait(&bars.o_free[st], ((phase >> (2 + st)) & 1) ^ 1)) return false;
-        if (v.y & kFirst) phase ^= 4u << st;
-        // while the weights are not there yet: the keys that follow, if they are
-        seen = more && __all_sync(0xffffffffu, mbar_test_wait(&bars.full[kp.stage], kp.round));
-        if (seen && !look(kp, qc, st, &k)) return false;
-        if (!wait(&bars.p_ready[st], (phase >> st) & 1)) return false;
-        phase ^= 1u << st;
-        tc_fence_after();
-        values(st, stage, v);
-        --todo;
-        // from the last dual tile's values to the first lone tile's: over K0 and K1
-        if (!(v.y & kPaired) || st == 1) vp.add(v.y & kLoneNext ? 3 : 2);
-      }
-      if (!more) continue;
-      if (!seen && (!wait(&bars.full[kp.stage], kp.round, a.wait_cycles) || !look(kp, qc, st, &k))) return false;
-      if (k.y & kEnd) {
-        more = false;
-        continue;
-      }
-      const bool paired = k.y & kPaired, done = !paired || st == 1;
-      scores(st, (qc + (paired ? st : 0)) & 1, kp.stage, k);
-      ++todo;
-      if (done) {
-        if (k.y & kLast) qc += paired ? 2 : 1;
-        kp.add(paired || lone ? 2 : 1);  // K1 comes right behind K0
-      }
-      lone = !paired;
+    Place<C::kKStages> kp;
+    Place<C::kVStages> vp;
+    if (!pairs) {  // tiles of one stream each: this one's first
+      kp.add(st);
+      vp.add(st);
     }
-    return true;
+    uint32_t tiles = 0, segments = 0, turns = 0;  // phases of p_ready, o_free, turn
+    const uint32_t s_tmem = same(tmem + st * 128), o_tmem = same(tmem + 256 + st * D);
+    bool started = false;
+    int2 v = make_int2(0, 0);
+    while (true) {
+      // the next keys
+      if (!wait(&bars.k_full[kp.stage], kp.round, a.wait_cycles)) return false;
+      const int2 k = bars.k_meta[kp.stage];
+      const bool more = !(k.y & kEnd);
+      const int q = (k.y / kQuery + (k.y & kPaired ? st : 0)) & 3;
+      if (more && (k.y & kFirst) && !wait(&bars.q_full[q & 1], q >> 1, a.wait_cycles)) return false;
+      const uint32_t kd = same((k_smem + kp.stage * C::kTile) >> 4), qd = same((q_smem + (q & 1) * C::kTile) >> 4);
+      const uint32_t sd = same(mma_desc(128, (k.x + 15) & ~15, false));
+      uint32_t vd = 0;
+      int steps = 0;
+      bool add = false;
+      if (started) {  // the values of the tile before
+        if (!wait(&bars.v_full[vp.stage], vp.round, a.wait_cycles)) return false;
+        v = bars.v_meta[vp.stage];
+        if ((v.y & kFirst) && !wait(&bars.o_free[st], (segments++ & 1) ^ 1)) return false;
+        vd = same((v_smem + vp.stage * C::kTile) >> 4);
+        steps = same((v.x + 15) / 16);
+        add = same(!(v.y & kFirst));
+        if (!wait(&bars.p_ready[st], tiles++ & 1)) return false;
+      }
+      if (!wait(&bars.turn[st], (turns++ & 1) ^ (st ^ 1))) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        if (started) {
+          constexpr uint32_t od = mma_desc(128, D, true);
+#pragma unroll
+          for (int x = 0; x < kKeys / 16; ++x) {
+            if (x >= steps) break;
+            mma_ts(o_tmem, s_tmem + x * 8, desc_of(vd + x * 128, C::kHalf), od, add || x > 0);
+            if (WIDE) mma_ts(o_tmem, s_tmem + 64 + x * 8, desc_of(vd + x * 128, C::kHalf), od, true);
+          }
+          mma_commit(&bars.v_empty[vp.stage]);
+          if (!(v.y & kPaired)) mma_commit(&bars.v_empty[vp.stage]);
+          if (v.y & kLast) mma_commit(&bars.o_full[st]);
+        }
+        if (more) {
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x) {
+            const uint32_t off = (x / 4 * C::kHalf + x % 4 * 32) >> 4;
+            mma_ss(s_tmem, desc_of(qd + off, 16), desc_of(kd + off, 16), sd, x > 0);
+          }
+        }
+        mbar_arrive(&bars.turn[st ^ 1]);
+        if (more) {
+          mma_commit(&bars.s_full[st]);
+          mma_commit(&bars.k_empty[kp.stage]);
+          if (!(k.y & kPaired)) mma_commit(&bars.k_empty[kp.stage]);
+          if (k.y & kLast) {
+            mma_commit(&bars.q_empty[q & 1]);
+            if (k.y & kAlone) mma_commit(&bars.q_empty[q & 1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (started) vp.add(v.y & kPaired ? step(v) : 2);
+      if (!more) return true;
+      started = true;
+      kp.add(k.y & kPaired ? step(k) : 2);
+    }
   }
+  // From a dual tile to this stream's next: the next, or behind the last of them its first lone tile.
+  __device__ __forceinline__ int step(int2 m) const { return m.y & kLoneNext ? 1 + st : 1; }
 };
 
 // ---- warps 0 to 7
@@ -372,7 +378,7 @@ struct Stream {
   const PrefixArgs& a;
   Bars& bars;
   const Waiter& wait;
-  char* ring;
+  char* ring;  // of values
   uint32_t ts, to;  // this warp's lanes of S and O
   int st, quarter, lane, r;
   uint32_t ns = 0, no = 0;
@@ -473,8 +479,8 @@ struct Stream {
       }
   }
 
-  // This stream's tiles j0, j0 + by, .. of a segment; v_at: ring place of tile 0's values, v_by from tile to tile.
-  __device__ __forceinline__ bool segment(const Segment& g, int j0, int by, uint32_t v_at, uint32_t v_by) {
+  // This stream's tiles j0, j0 + by, .. of a segment that starts with the share's tile `tile0`.
+  __device__ __forceinline__ bool segment(const Segment& g, int j0, int by, uint32_t tile0) {
     const PrefixShape& s = a.s;
     const int n = g.t1 - g.t0;
     const int parts = g.kind == kOwn ? s.own_parts : g.kind == kSingle ? s.prefix_parts : 1;
@@ -515,9 +521,9 @@ struct Stream {
       if (!wait(&bars.s_full[st], ns++ & 1)) return false;
       tc_fence_after();
       if (left & 15) {  // rows of V behind the sequence, up to the end of the last MMA's 16
-        const uint32_t p = v_at + v_by * j;
-        const int stage = p % C::kStages;
-        if (!wait(&bars.full[stage], (p / C::kStages) & 1)) return false;
+        const uint32_t p = tile0 + j;
+        const int stage = p % C::kVStages;
+        if (!wait(&bars.v_full[stage], (p / C::kVStages) & 1)) return false;
         if (r >= left && r < ((left + 15) & ~15)) {
           char* v = ring + stage * C::kTile + r * 128;
 #pragma unroll
@@ -567,15 +573,14 @@ struct Stream {
 
   __device__ __forceinline__ bool run(Walk walk, int cta) {
     Segment g;
-    uint32_t base = 0, x = 0;  // ring places of the dual tiles so far, single and own tiles so far
+    uint32_t tile = 0;
+    int turn = 0;  // whose tile the next single or own one is
     while (walk.next(a, cta, &g)) {
       const bool dual = g.kind == kDual;
-      const int n = g.t1 - g.t0, j0 = dual ? 0 : (st ^ x) & 1;
-      if (j0 < n && !segment(g, j0, dual ? 1 : 2, base + (dual ? 1 : 2 * x + 2), 2)) return false;
-      if (dual)
-        base += 2 * n;
-      else
-        x += n;
+      const int n = g.t1 - g.t0, j0 = dual ? 0 : st ^ turn;
+      if (j0 < n && !segment(g, j0, dual ? 1 : 2, tile)) return false;
+      tile += n;
+      if (!dual) turn ^= n & 1;
     }
     return true;
   }
@@ -587,25 +592,28 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
   using C = Tc<D>;
   const PrefixArgs& a = args.a;
   char* base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
-  Bars& bars = *reinterpret_cast<Bars*>(base + (2 + C::kStages) * C::kTile);
-  const uint32_t q_smem = smem_addr(base), kv_smem = q_smem + 2 * C::kTile;
+  Bars& bars = *reinterpret_cast<Bars*>(base + (2 + C::kKStages + C::kVStages) * C::kTile);
+  const uint32_t q_smem = smem_addr(base);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
   const Waiter wait{a.v.err, &bars.gone};
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&bars.full[i], 1);
-      mbar_init(&bars.empty[i], 1);
+    for (int i = 0; i < 5; ++i) {
+      mbar_init(&bars.k_full[i], 1);
+      mbar_init(&bars.k_empty[i], 2);
+      mbar_init(&bars.v_full[i], 1);
+      mbar_init(&bars.v_empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.q_full[i], 1);
-      mbar_init(&bars.q_empty[i], 1);
+      mbar_init(&bars.q_empty[i], 2);
       mbar_init(&bars.s_full[i], 1);
       mbar_init(&bars.p_ready[i], 4);
       mbar_init(&bars.o_full[i], 1);
       mbar_init(&bars.o_free[i], 4);
+      mbar_init(&bars.turn[i], 1);
+      mbar_init(&bars.drain[i], 1);
     }
-    mbar_init(&bars.drain, 1);
     bars.gone = 0;
     fence_mbar_init();
   }
@@ -621,25 +629,23 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
 
   if (warp < 8) {
     more_registers<kStreamRegs>();
-    Stream<D, WIDE> s(args, bars, wait, base + 2 * C::kTile, tmem);
+    Stream<D, WIDE> s(args, bars, wait, base + (2 + C::kKStages) * C::kTile, tmem);
     s.run(walk, cta);
   } else {
     fewer_registers<kOtherRegs>();
     if (warp == 8) {
-      Loader<D> x(args, bars, wait, q_smem, kv_smem);
-      if (!x.run(walk, cta)) {  // leave no load in flight
-        for (uint32_t i = x.at.index > C::kStages ? x.at.index - C::kStages : 0; i < x.at.index; ++i)
-          mbar_wait_bounded(&bars.full[i % C::kStages], (i / C::kStages) & 1, a.v.err, kDevErrTimeout, kCopyWaitCycles);
-        for (uint32_t i = x.qc > 2 ? x.qc - 2 : 0; i < x.qc; ++i)
-          mbar_wait_bounded(&bars.q_full[i & 1], (i >> 1) & 1, a.v.err, kDevErrTimeout, kCopyWaitCycles);
-      }
+      Loader<D> x(args, bars, wait, q_smem, q_smem + 2 * C::kTile);
+      if (!x.template run<true>(walk, cta)) x.template drain<true>();
     } else if (warp == 9) {
-      Issuer<D, WIDE> x(args, bars, wait, q_smem, kv_smem, tmem);
+      Loader<D> x(args, bars, wait, q_smem, q_smem + (2 + C::kKStages) * C::kTile);
+      if (!x.template run<false>(walk, cta)) x.template drain<false>();
+    } else {
+      Issuer<D, WIDE> x(args, bars, wait, q_smem, tmem, warp - 10);
       x.run(walk.pos < walk.hi && walk.pos < a.s.dual_total);
       // leave no MMA in flight, whatever ended the run
-      if (elect_one()) mma_commit(&bars.drain);
+      if (elect_one()) mma_commit(&bars.drain[warp - 10]);
       __syncwarp();
-      mbar_wait_bounded(&bars.drain, 0, a.v.err, kDevErrTimeout, kCopyWaitCycles);
+      mbar_wait_bounded(&bars.drain[warp - 10], 0, a.v.err, kDevErrTimeout, kCopyWaitCycles);
     }
   }
   __syncwarp();

@@ -92,6 +92,10 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
       ZHA_W8(r, 0), ZHA_W8(r, 8)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), ZHA_W8(r, 0)
+               : "memory");
+}
 #undef ZHA_R8
 #undef ZHA_W8
 
@@ -138,7 +142,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
-__device__ __forceinline__ uint64_t neg2(uint64_t a) { return a ^ 0x8000000080000000ull; }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -153,7 +156,7 @@ __device__ __forceinline__ void exp2_by_fma(uint64_t x, float* lo, float* hi) {
   split(x, &a, &b);
   x = pair(fmaxf(a, -126.f), fmaxf(b, -126.f));
   const uint64_t n = add2(x, pair(12582912.f, 12582912.f));
-  const uint64_t f = add2(x, neg2(add2(n, pair(-12582912.f, -12582912.f))));
+  const uint64_t f = fma2(add2(n, pair(-12582912.f, -12582912.f)), pair(-1.f, -1.f), x);
   uint64_t p = fma2(f, pair(kExp2C3, kExp2C3), pair(kExp2C2, kExp2C2));
   p = fma2(f, p, pair(kExp2C1, kExp2C1));
   p = fma2(f, p, pair(kExp2C0, kExp2C0));
