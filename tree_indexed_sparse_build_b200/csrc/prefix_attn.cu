@@ -222,29 +222,41 @@ __global__ void __launch_bounds__(kThreads, 2) fp32_kernel(const __grid_constant
 
 // ---------------------------------------------------------------- join
 //
-// One CTA per output row: its warps take the row's partial results in turn, rescale by the
-// maxima and add (fp32); the order is fixed, so the result does not depend on timing.
-constexpr int kJoinWarps = 8;
+// One CTA for up to four rows of a sequence and head: its warps take the rows' partial results in turn (finding one
+// takes longer than reading it, and it is found for all the rows at once), rescale by the maxima and
+// add (fp32); the order is fixed, so the result does not depend on timing.
+constexpr int kJoinWarps = 8, kJoinRows = 4, kAtOnce = 2;
 
 template <int D>
 struct Joined {
-  float m = -INFINITY, l = 0.f, acc[D / 32];
+  static constexpr int N = D / 32;  // columns of a lane
+  float m = -INFINITY, l = 0.f, acc[N];
   __device__ __forceinline__ Joined() {
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) acc[c] = 0.f;
+    for (int c = 0; c < N; ++c) acc[c] = 0.f;
   }
-  __device__ __forceinline__ void add(float pm, float pl, const float* px) {
-    const float top = fmaxf(m, pm);
-    if (top == -INFINITY) return;
-    const float x = exp2f(m - top), y = exp2f(pm - top);
-    m = top;
-    l = l * x + pl * y;
+  template <int K>
+  __device__ __forceinline__ void add(const float2 (&ml)[K], const float (&x)[K][N]) {
+    float top = m;
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) acc[c] = acc[c] * x + px[c] * y;
+    for (int k = 0; k < K; ++k) top = fmaxf(top, ml[k].x);
+    if (top == -INFINITY) return;
+    float f = exp2f(m - top);
+    m = top;
+    l *= f;
+#pragma unroll
+    for (int c = 0; c < N; ++c) acc[c] *= f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      f = exp2f(ml[k].x - top);
+      l += ml[k].y * f;
+#pragma unroll
+      for (int c = 0; c < N; ++c) acc[c] += x[k][c] * f;
+    }
   }
 };
 
-// The CTA whose share of T holds key tile x.
+// The CTA whose share of T holds position x.
 __device__ __forceinline__ int cta_of(int x, int T, int ctas) {
   const int each = T / ctas, more = T - each * ctas, bent = more * (each + 1);
   return x < bent ? x / (each + 1) : more + (x - bent) / each;
@@ -252,39 +264,54 @@ __device__ __forceinline__ int cta_of(int x, int T, int ctas) {
 
 template <int D, typename TO>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ PrefixArgs a) {
-  __shared__ float s_acc[kJoinWarps][D];
-  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
+  using J = Joined<D>;
+  __shared__ float s_acc[kJoinRows][kJoinWarps][D];
+  __shared__ float2 s_ml[kJoinRows][kJoinWarps];
   pdl_wait();
   pdl_release();
   const PrefixShape& s = a.s;
-  const long long at = blockIdx.x;  // (sequence, head, row)
-  const int rem = (int)(at % s.rows), head = (int)(at / s.rows % s.heads), b = (int)(at / s.rows / s.heads);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int chunks = (s.rows + kJoinRows - 1) / kJoinRows;
+  const int bh = blockIdx.x / chunks, head = bh % s.heads, b = bh / s.heads;
+  const int rem = (blockIdx.x - bh * chunks) * kJoinRows, rows = min(kJoinRows, s.rows - rem);  // row tiles are multiples of 4 rows
   const int group = s.heads * s.own_tiles;
-  const int T = s.prefix_total + a.cum[s.batch] * group;
-  Joined<D> sum;
-  auto take = [&](long long row) {
-    const float2 x = a.ml[row];
-    float y[D / 32];
-    if (D == 128) {
-      const float4 z = *reinterpret_cast<const float4*>(a.acc + row * D + 4 * lane);
-      y[0] = z.x, y[1] = z.y, y[D / 32 - 2] = z.z, y[D / 32 - 1] = z.w;
-    } else {
-      const float2 z = *reinterpret_cast<const float2*>(a.acc + row * D + 2 * lane);
-      y[0] = z.x, y[1] = z.y;
-    }
-    sum.add(x.x, x.y, y);
-  };
-  // the partial results of the segments of an item of n key tiles at `start`: `parts` rows `step` apart
-  // of each stream that took part
-  auto item = [&](int start, int n, int streams, int parts, long long slot0, int slot_rows, int step) {
-    const int c0 = cta_of(start, T, s.ctas), c1 = cta_of(start + n - 1, T, s.ctas);
-    const int each = streams * parts;
-    for (int i = warp; i < (c1 - c0 + 1) * each; i += kJoinWarps) {
-      const int c = c0 + i / each, k = i % each;
-      const int tiles = min(start + n, share_start(c + 1, T, s.ctas)) - max(start, share_start(c, T, s.ctas));
-      if (tiles <= k / parts) continue;
-      take(slot0 + (long long)c * slot_rows + k * step);
+  const int before = a.cum[b], all = a.cum[s.batch], len = a.cum[s.batch + 1 + b];
+  const bool lost = (*a.v.err & kDevErrTimeout) != 0;
+  const int T = s.prefix_total + all * group;
+  J sum[kJoinRows];
+  // the partial results of the segments of an item of n key tiles of cost w from `start`: `parts` rows
+  // `step` apart of each stream that took part
+  auto item = [&](int start, int n, int w, int streams, int parts, long long slot0, int slot_rows, int step) {
+    const int c0 = cta_of(start, T, s.ctas), c1 = cta_of(start + (n - 1) * w, T, s.ctas);
+    const int each = streams * parts, count = (c1 - c0 + 1) * each;
+    for (int i0 = warp; i0 < count; i0 += kJoinWarps * kAtOnce) {
+      float2 ml[kJoinRows][kAtOnce];
+      float x[kJoinRows][kAtOnce][J::N];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int i = i0 + u * kJoinWarps, y = i / each, c = c0 + y, k = i - y * each;
+        const int lo = share_start(c, T, s.ctas), hi = share_start(c + 1, T, s.ctas);
+        const bool there = i < count && tiles_before(hi, start, n, w) - tiles_before(lo, start, n, w) > (parts == 1 ? k : k / parts);
+        const long long row = slot0 + (long long)c * slot_rows + k * step;
+#pragma unroll
+        for (int r = 0; r < kJoinRows; ++r) {
+          ml[r][u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+          for (int q = 0; q < J::N; ++q) x[r][u][q] = 0.f;
+          if (!there || r >= rows) continue;
+          ml[r][u] = a.ml[row + r];
+          const float* p = a.acc + (row + r) * D + J::N * lane;
+          if constexpr (D == 128) {
+            const float4 z = *reinterpret_cast<const float4*>(p);
+            x[r][u][0] = z.x, x[r][u][1] = z.y, x[r][u][2] = z.z, x[r][u][3] = z.w;
+          } else {
+            const float2 z = *reinterpret_cast<const float2*>(p);
+            x[r][u][0] = z.x, x[r][u][1] = z.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < kJoinRows; ++r) sum[r].add(ml[r], x[r]);
     }
   };
   if (s.prefix > 0) {
@@ -298,47 +325,53 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     }
     if (rt < 2 * s.duals) {
       const int x = head * s.duals + (rt >> 1);
-      item(x * s.prefix_keys, s.prefix_keys, 1, 1, (long long)x * s.dual_slot_rows + (rt & 1) * s.prefix_tile + r, s.dual_slot_rows, 0);
+      item(x * s.prefix_keys * kDualCost, s.prefix_keys, kDualCost, 1, 1, (long long)x * s.dual_slot_rows + (rt & 1) * s.prefix_tile + r, s.dual_slot_rows, 0);
     } else {
       const int x = head * s.singles + rt - 2 * s.duals;
-      item(s.dual_total + x * s.prefix_keys, s.prefix_keys, s.streams, s.prefix_parts, s.single_slot0 + (long long)x * s.single_slot_rows + r, s.single_slot_rows,
+      item(s.dual_total + x * s.prefix_keys * kTileCost, s.prefix_keys, kTileCost, s.streams, s.prefix_parts, s.single_slot0 + (long long)x * s.single_slot_rows + r, s.single_slot_rows,
            s.single_slot_rows / (s.streams * s.prefix_parts));
     }
   }
-  int slot;
-  const int len = prefix_len(a, b, &slot);
   const int n = own_key_tiles(s, len);
   if (n > 0) {
     const int x = head * s.own_tiles + rem / s.own_tile;
-    item(s.prefix_total + a.cum[b] * group + x * (n + kOwnStart) + kOwnStart, n, s.streams, s.own_parts,
+    item(s.prefix_total + before * group + x * own_cost(s, len) + kOwnStart, n, kTileCost, s.streams, s.own_parts,
          s.own_slot0 + ((long long)b * group + x) * s.own_slot_rows + rem % s.own_tile, s.own_slot_rows,
          s.own_slot_rows / (s.streams * s.own_parts));
   }
-  if (lane == 0) {
-    s_m[warp] = sum.m;
-    s_l[warp] = sum.l;
+#pragma unroll
+  for (int r = 0; r < kJoinRows; ++r) {
+    if (lane == 0) s_ml[r][warp] = make_float2(sum[r].m, sum[r].l);
+#pragma unroll
+    for (int c = 0; c < J::N; ++c) s_acc[r][warp][lane * J::N + c] = sum[r].acc[c];
   }
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c) s_acc[warp][lane * (D / 32) + c] = sum.acc[c];
   __syncthreads();
-  if (warp != 0) return;
-  Joined<D> all;
+  if (warp >= rows) return;
+  float2 ml[kJoinWarps];
+  float x[kJoinWarps][J::N];
 #pragma unroll
-  for (int i = 0; i < kJoinWarps; ++i) all.add(s_m[i], s_l[i], &s_acc[i][lane * (D / 32)]);
-  const bool sees = tokens_seen(s, len, rem % s.nq) > 0;
-  const bool lost = (*a.v.err & kDevErrTimeout) != 0;
-  TO* O = static_cast<TO*>(a.O) + at * D + lane * (D / 32);
+  for (int i = 0; i < kJoinWarps; ++i) {
+    ml[i] = s_ml[warp][i];
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c) {
-    const float x = lost ? NAN : sees ? all.acc[c] / all.l : 0.f;
+    for (int c = 0; c < J::N; ++c) x[i][c] = s_acc[warp][i][lane * J::N + c];
+  }
+  J row;
+  row.add(ml, x);
+  const bool sees = tokens_seen(s, len, (rem + warp) % s.nq) > 0;
+  TO* O = static_cast<TO*>(a.O) + ((size_t)bh * s.rows + rem + warp) * D + lane * J::N;
+#pragma unroll
+  for (int c = 0; c < J::N; ++c) {
+    const float y = lost ? NAN : sees ? row.acc[c] / row.l : 0.f;
     if constexpr (sizeof(TO) == 2)
-      O[c] = f32_to_bf16_bits(x);
+      O[c] = f32_to_bf16_bits(y);
     else
-      O[c] = x;
+      O[c] = y;
   }
 }
 
 // ---------------------------------------------------------------- host
+
+int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 template <int D, typename TQ, typename TKV>
 cudaError_t launch_fp32(const PrefixArgs& a, cudaStream_t s) {
@@ -357,14 +390,12 @@ cudaError_t launch_fp32_types(const PrefixArgs& a, zha_dtype q, zha_dtype kv, cu
 
 template <int D>
 cudaError_t launch_join(const PrefixArgs& a, zha_dtype o, cudaStream_t s) {
-  const dim3 grid((unsigned)((long long)a.s.batch * a.s.heads * a.s.rows)), block(kJoinWarps * 32);
+  const dim3 grid((unsigned)((long long)a.s.batch * a.s.heads * ceil_div(a.s.rows, kJoinRows))), block(kJoinWarps * 32);
   return o == ZHA_BF16 ? launch_pdl(join_kernel<D, uint16_t>, grid, block, 0, s, a)
                        : launch_pdl(join_kernel<D, float>, grid, block, 0, s, a);
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 // The cut of a call.  Returns false on sizes outside the kernels' index ranges.
 bool plan(const zha_pages* p, int batch, int q_heads, int nq, long long prefix, bool tensor, PrefixShape* s) {
@@ -400,13 +431,13 @@ bool plan(const zha_pages* p, int batch, int q_heads, int nq, long long prefix, 
   s->prefix_parts = tensor && rows * batch <= 32 ? 4 : 1;
   s->own_parts = tensor && rows <= 32 ? 4 : 1;
   s->ctas = tensor ? p->sms : 2 * p->sms;
-  // all key tiles, sequences as long as they may be, are counted in 31 bits
+  // all costs, sequences as long as they may be, are counted in 31 bits
   const long long most = (long long)p->desc.max_seq_pages * p->desc.page_tokens;
-  if ((long long)heads * row_tiles * s->prefix_keys +
-          (long long)batch * heads * s->own_tiles * (ceil_div(most, s->tile_keys) + kOwnStart) > 0x7fffffffLL)
+  if ((long long)heads * row_tiles * s->prefix_keys * kDualCost +
+          (long long)batch * heads * s->own_tiles * (ceil_div(most, s->tile_keys) * kTileCost + kOwnStart) > 0x7fffffffLL)
     return false;
-  s->dual_total = heads * s->duals * s->prefix_keys;
-  s->prefix_total = s->dual_total + heads * s->singles * s->prefix_keys;
+  s->dual_total = heads * s->duals * s->prefix_keys * kDualCost;
+  s->prefix_total = s->dual_total + heads * s->singles * s->prefix_keys * kTileCost;
   s->dual_slot_rows = 2 * s->prefix_tile;
   const int single_rows = s->prefix_parts == 4 ? (int)rows * batch : s->prefix_tile;
   s->single_slot_rows = s->streams * s->prefix_parts * single_rows;
@@ -430,7 +461,7 @@ Scratch scratch_of(const zha_pages* p, const PrefixShape& s) {
       s.own_slot0 + ((long long)s.batch * s.heads * s.own_tiles + s.ctas) * s.own_slot_rows;
   Scratch x;
   x.cum = 0;
-  x.ml = ((size_t)(s.batch + 1) * 4 + 255) / 256 * 256;
+  x.ml = ((size_t)(2 * s.batch + 1) * 4 + 255) / 256 * 256;
   x.acc = x.ml + ((size_t)rows * 8 + 255) / 256 * 256;
   x.bytes = x.acc + (size_t)rows * p->desc.head_dim * 4;
   return x;

@@ -6,11 +6,10 @@
 //           tokens (tensor kernel only: its two streams share the loads)
 //   single  one row tile against the shared tokens
 //   own     one sequence's rows (or a slice) against its tokens behind the prefix
-// All items' key tiles, laid end to end in that order, are cut into one equal share per CTA, so that
-// no CTA waits for a long sequence.  The kinds' tiles cost about the same, their 64 KB of keys and values;
-// an own item counts for one tile more, for its start and end.  A CTA's part of an item is a segment; its
-// result (maximum, sum and weighted values, fp32) goes to the slot item + cta, which is unique
-// because both only grow along the order.  A second kernel joins a row's slots.
+// All items, laid end to end in that order, are cut into one equal share of cost per CTA, so that no CTA
+// waits for a long sequence; a key tile belongs to the share in which it starts.  A CTA's part of an
+// item is a segment; its result (maximum, sum and weighted values, fp32) goes to the slot item + cta,
+// which is unique because both only grow along the order.  A second kernel joins a row's slots.
 //
 // The cut depends on lengths that only the device knows.  A CTA finds its place by a sum
 // over the batch's lengths; the join finds a row's segments by arithmetic on the same sums.
@@ -38,7 +37,7 @@ struct PrefixShape {
   int streams;         // streams of a single or own item's segment (1, or 2 in the tensor kernel)
   int prefix_keys;     // key tiles of the prefix
   int ctas;
-  int dual_total, prefix_total;  // key tiles of all dual items, of all prefix items
+  int dual_total, prefix_total;  // cost of all dual items, of all prefix items
   int dual_slot_rows, single_slot_rows, own_slot_rows;
   long long single_slot0, own_slot0;   // first row of the single and of the own slots
 };
@@ -50,7 +49,7 @@ struct PrefixArgs {
   const void* K;
   const void* V;
   const int* seqs;
-  int* cum;        // [batch + 1] own cost before a sequence, per row tile (written by CTA 0 for the join)
+  int* cum;        // [batch + 1] own cost before a sequence, per row tile, and [batch] tokens (by CTA 0, for the join)
   float2* ml;      // [slot rows] maximum (base 2, scaled) and sum
   float* acc;      // [slot rows, head_dim]
   void* O;
@@ -75,13 +74,20 @@ __device__ __forceinline__ int tokens_seen(const PrefixShape& s, int len, int i)
   return s.causal ? len - s.nq + 1 + i : len;
 }
 
-// The first key tile of CTA c's share of T (c == ctas: T).
+// Costs, by what the tensor kernel takes: a dual tile about 3,900 clocks, any other, which its 64 KB of keys
+// and values bound, about 2,600, and so does an own item's start and end.
+constexpr int kDualCost = 3, kTileCost = 2, kOwnStart = 2;
+
+// Where CTA c's share of the cost T starts (c == ctas: T).
 __device__ __forceinline__ int share_start(int c, int T, int ctas) {
   const int each = T / ctas, more = T - each * ctas;
   return c * each + min(c, more);
 }
 
-constexpr int kOwnStart = 1;  // what an own item costs besides its tiles
+// Of n tiles of cost w from position `at`, those that start before x.
+__device__ __forceinline__ int tiles_before(int x, int at, int n, int w) {
+  return max(0, min(n, (x - at + w - 1) / w));
+}
 
 enum SegmentKind { kDual = 0, kSingle = 1, kOwn = 2 };
 
@@ -102,7 +108,7 @@ struct Walk {
   int b, n;             // own part: the sequence at pos and its key tiles
   int len, pages;       // its tokens and slot
   int next_len, next_pages;  // those of sequence b + 1, fetched ahead
-  int item, t;          // its row tile (heads * own_tiles of them), and its key tile at pos; below 0: in its start
+  int item, at;         // its row tile (heads * own_tiles of them), and where that item's first key tile starts
 
   __device__ __forceinline__ void fetch(const PrefixArgs& a) {
     next_len = 0;
@@ -111,13 +117,14 @@ struct Walk {
 
   __device__ __forceinline__ bool next(const PrefixArgs& a, int cta, Segment* g) {
     const PrefixShape& s = a.s;
-    if (pos >= hi) return false;
-    if (pos < s.prefix_total) {
+    while (pos < hi && pos < s.prefix_total) {
       const bool dual = pos < s.dual_total;
-      const int per_head = dual ? s.duals : s.singles, origin = dual ? 0 : s.dual_total;
-      const int i = (pos - origin) / s.prefix_keys;
-      g->t0 = pos - origin - i * s.prefix_keys;
-      g->t1 = min(s.prefix_keys, g->t0 + hi - pos);
+      const int w = dual ? kDualCost : kTileCost, per_head = dual ? s.duals : s.singles, origin = dual ? 0 : s.dual_total;
+      const int len_w = s.prefix_keys * w, i = (pos - origin) / len_w, start = origin + i * len_w;
+      g->t0 = tiles_before(pos, start, s.prefix_keys, w);
+      g->t1 = tiles_before(hi, start, s.prefix_keys, w);
+      pos = start + len_w;
+      if (g->t0 >= g->t1) continue;
       g->kind = dual ? kDual : kSingle;
       g->head = i / per_head;
       g->tile = dual ? 2 * (i - g->head * per_head) : 2 * s.duals + i - g->head * per_head;
@@ -125,47 +132,46 @@ struct Walk {
       g->pages = s.prefix_seq;
       g->len = s.prefix;
       g->slot = dual ? (long long)(i + cta) * s.dual_slot_rows : s.single_slot0 + (long long)(i + cta) * s.single_slot_rows;
-      pos += g->t1 - g->t0;
       return true;
     }
     const int group = s.heads * s.own_tiles;
-    if (t == n) {  // the next item
-      t = -kOwnStart;
-      if (++item == group) {
-        item = 0;
-        do {
-          ++b;
-          len = next_len;
-          pages = next_pages;
-          n = own_key_tiles(s, len);
-          fetch(a);
-        } while (n == 0 && b < s.batch);
-        if (b >= s.batch) return false;
+    while (pos < hi) {
+      const int end = at + n * kTileCost;
+      if (pos >= end) {  // the next item
+        if (++item == group) {
+          item = 0;
+          do {
+            ++b;
+            len = next_len;
+            pages = next_pages;
+            n = own_key_tiles(s, len);
+            fetch(a);
+          } while (n == 0 && b < s.batch);
+          if (b >= s.batch) return false;
+        }
+        at = end + kOwnStart;
+        continue;
       }
+      g->t0 = tiles_before(pos, at, n, kTileCost);
+      g->t1 = tiles_before(hi, at, n, kTileCost);
+      pos = end;
+      if (g->t0 >= g->t1) continue;
+      g->kind = kOwn;
+      g->head = s.own_tiles == 1 ? item : item / s.own_tiles;
+      g->tile = item - g->head * s.own_tiles;
+      g->b = b;
+      g->pages = pages;
+      g->len = len;
+      g->slot = s.own_slot0 + ((long long)b * group + item + cta) * s.own_slot_rows;
+      return true;
     }
-    if (t < 0) {
-      pos -= t;
-      t = 0;
-      if (pos >= hi) return false;
-    }
-    g->t0 = t;
-    g->t1 = min(n, t + hi - pos);
-    g->kind = kOwn;
-    g->head = s.own_tiles == 1 ? item : item / s.own_tiles;
-    g->tile = item - g->head * s.own_tiles;
-    g->b = b;
-    g->pages = pages;
-    g->len = len;
-    g->slot = s.own_slot0 + ((long long)b * group + item + cta) * s.own_slot_rows;
-    pos += g->t1 - t;
-    t = g->t1;
-    return true;
+    return false;
   }
 };
 
 __device__ __forceinline__ int own_cost(const PrefixShape& s, int len) {
   const int n = own_key_tiles(s, len);
-  return n ? n + kOwnStart : 0;
+  return n ? n * kTileCost + kOwnStart : 0;
 }
 
 // Finds CTA `cta`'s share; all of the CTA's `threads` threads call it.  sm: at least
@@ -185,7 +191,10 @@ __device__ __forceinline__ Walk find_share(const PrefixArgs& a, int cta, int thr
       len_first = len;
       slot_first = slot;
     }
-    if (cta == 0 && (unsigned)slot >= (unsigned)a.v.max_seqs) atomicOr(a.v.err, kDevErrBadSeq);
+    if (cta == 0) {
+      a.cum[s.batch + 1 + b] = len;
+      if ((unsigned)slot >= (unsigned)a.v.max_seqs) atomicOr(a.v.err, kDevErrBadSeq);
+    }
   }
   mine = __reduce_add_sync(0xffffffffu, mine);
   if (lane == 0) sm[warp] = mine;
@@ -196,7 +205,7 @@ __device__ __forceinline__ Walk find_share(const PrefixArgs& a, int cta, int thr
   Walk w;
   w.pos = share_start(cta, T, s.ctas);
   w.hi = share_start(cta + 1, T, s.ctas);
-  w.b = w.n = w.item = w.t = w.len = w.pages = w.next_len = w.next_pages = 0;
+  w.b = w.n = w.item = w.at = w.len = w.pages = w.next_len = w.next_pages = 0;
   if (cta == 0 && tid == 0) {
     a.cum[s.batch] = total;
     if (s.prefix > 0 && a.v.lens[s.prefix_seq] < s.prefix) atomicOr(a.v.err, kDevErrBadSeq);
@@ -240,9 +249,9 @@ __device__ __forceinline__ Walk find_share(const PrefixArgs& a, int cta, int thr
       w.len = out[2];
       w.pages = out[3];
       w.n = own_key_tiles(s, w.len);
-      const int y = x - out[1] * group, cost = w.n + kOwnStart;
-      w.item = y / cost;
-      w.t = y - w.item * cost - kOwnStart;
+      const int before = out[1] * group, cost = w.n * kTileCost + kOwnStart;
+      w.item = (x - before) / cost;
+      w.at = s.prefix_total + before + w.item * cost + kOwnStart;
       w.fetch(a);
     }
     __syncthreads();

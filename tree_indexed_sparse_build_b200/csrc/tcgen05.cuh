@@ -79,6 +79,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t* r, uint32_t addr) {
       : ZHA_R8(r, 0), ZHA_R8(r, 8), ZHA_R8(r, 16), ZHA_R8(r, 24)
       : "r"(addr));
 }
+// 64 columns of 16 lanes from `addr`'s on, as 8 blocks of 8 columns: block j of thread t is columns 8 j + 2 (t % 4) + 0, 1 of
+// lane t / 4 (r[4 j], r[4 j + 1]) and of lane t / 4 + 8 (r[4 j + 2], r[4 j + 3]); four threads hold 32 bytes of a lane.
+__device__ __forceinline__ void tmem_ld_blocks(uint32_t* r, uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : ZHA_R8(r, 0), ZHA_R8(r, 8), ZHA_R8(r, 16), ZHA_R8(r, 24)
+      : "r"(addr));
+}
 __device__ __forceinline__ void tmem_ld16(uint32_t* r, uint32_t addr) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
