@@ -168,6 +168,14 @@ def test_random_shapes():
              prefix_seq=0 if lens[0] >= prefix else (lens + [prefix]).index(max(lens + [prefix])), seed=seed)
 
 
+@pytest.mark.parametrize("keys", [1, 3, 5, 9, 13, 21, 32])
+def test_shares_that_start_inside_the_last_tile_of_a_kind(keys):
+    # two row tiles against `keys` key tiles, then own parts: at these lengths some CTA's share starts inside the
+    # last tile of the shared part (cut for 148 CTAs), which is the CTA's before
+    prefix = 128 * keys
+    _run(_zha(), 2, 8, 64, 128, prefix, [prefix + 130 * (1 + i % 3) for i in range(32)], 1, False, BF16, BF16, BF16)
+
+
 def test_bad_slots_pages_and_prefixes_are_reported():
     zha = _zha()
     for kv in (F32, BF16):

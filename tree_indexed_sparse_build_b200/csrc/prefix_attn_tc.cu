@@ -38,7 +38,7 @@ namespace {
 constexpr int kRows = 128, kKeys = 128;
 constexpr int kThreads = 384;
 constexpr int kTmemCols = 512;
-constexpr int kByFma = 3;     // of 16 pairs of weights, those whose exp2 the FMA pipes compute
+constexpr int kByFma = 2;     // of 16 pairs of weights, those whose exp2 the FMA pipes compute
 constexpr float kSlack = 8.f;  // base-2 growth of the maximum that is let pass
 
 struct TcMaps {
@@ -57,7 +57,7 @@ template <int D>
 struct Tc {
   static constexpr int kTile = 128 * D * 2;  // bytes of 128 rows
   static constexpr int kHalf = 128 * 128;    // bytes of 128 rows x 64 elements
-  static constexpr int kKStages = D == 128 ? 3 : 5, kVStages = D == 128 ? 2 : 5;
+  static constexpr int kKStages = D == 128 ? 2 : 5, kVStages = D == 128 ? 3 : 5;
   static constexpr size_t kSmem = 1024 + (size_t)(2 + kKStages + kVStages) * kTile + 1024;
 };
 
@@ -655,7 +655,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
       if (!x.template run<false>(walk, cta)) x.template drain<false>();
     } else {
       Issuer<D, WIDE> x(args, bars, wait, q_smem, tmem, warp - 10);
-      x.run(walk.pos < walk.hi && walk.pos < a.s.dual_total);
+      // (a share may start inside the last dual tile, which is the one before's)
+      Walk w = walk;
+      Segment first;
+      x.run(w.next(a, cta, &first) && first.kind == kDual);
       // leave no MMA in flight, whatever ended the run
       if (elect_one()) mma_commit(&bars.drain[warp - 10]);
       __syncwarp();
