@@ -168,7 +168,7 @@ def test_random_shapes():
              prefix_seq=0 if lens[0] >= prefix else (lens + [prefix]).index(max(lens + [prefix])), seed=seed)
 
 
-@pytest.mark.parametrize("keys", [1, 3, 5, 9, 13, 21, 32])
+@pytest.mark.parametrize("keys", [1, 3, 5, 13, 16, 19, 25, 32, 40, 50])
 def test_shares_that_start_inside_the_last_tile_of_a_kind(keys):
     # two row tiles against `keys` key tiles, then own parts: at these lengths some CTA's share starts inside the
     # last tile of the shared part (cut for 148 CTAs), which is the CTA's before

@@ -74,9 +74,9 @@ __device__ __forceinline__ int tokens_seen(const PrefixShape& s, int len, int i)
   return s.causal ? len - s.nq + 1 + i : len;
 }
 
-// Costs, by what the tensor kernel takes: a dual tile about 3,900 clocks, any other, which its 64 KB of keys
-// and values bound, about 2,600, and so does an own item's start and end.
-constexpr int kDualCost = 3, kTileCost = 2, kOwnStart = 2;
+// Costs, by what the tensor kernel takes: a dual tile about 3,900 clocks, any other (its 64 KB of keys
+// and values are the bound) 2,000 to 2,600, and so does the start and end of an own item.
+constexpr int kDualCost = 2, kTileCost = 1, kOwnStart = 1;
 
 // Where CTA c's share of the cost T starts (c == ctas: T).
 __device__ __forceinline__ int share_start(int c, int T, int ctas) {

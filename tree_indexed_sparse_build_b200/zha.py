@@ -461,10 +461,18 @@ def zha_pages_workspace_bytes(desc: zha_pages_desc) -> int:
     return int(lib().zha_pages_workspace_bytes(ctypes.byref(desc)))
 
 
-def zha_pages_init(desc: zha_pages_desc, workspace: torch.Tensor, stream=None) -> ctypes.c_void_p:
-    h = ctypes.c_void_p()
+class _PagesHandle(ctypes.c_void_p):
+    """A zha_pages handle that knows its geometry and device: they never change, and asking the
+    library again at every call would cost a small call a fifth of its time."""
+    desc: zha_pages_desc | None = None
+    device: int | None = None
+
+
+def zha_pages_init(desc: zha_pages_desc, workspace: torch.Tensor, stream=None) -> _PagesHandle:
+    h = _PagesHandle()
     _check(lib().zha_pages_init(ctypes.byref(desc), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                 _stream(stream), ctypes.byref(h)), "zha_pages_init")
+    h.desc, h.device = zha_pages_get_desc(h), zha_pages_device(h)
     return h
 
 
@@ -473,13 +481,17 @@ def zha_pages_destroy(handle) -> None:
 
 
 def zha_pages_get_desc(handle) -> zha_pages_desc:
+    d = getattr(handle, "desc", None)
+    if d is not None:
+        return d
     d = zha_pages_desc()
     _check(lib().zha_pages_get_desc(handle, ctypes.byref(d)), "zha_pages_get_desc")
     return d
 
 
 def zha_pages_device(handle) -> int:
-    return int(lib().zha_pages_device(handle))
+    d = getattr(handle, "device", None)
+    return int(lib().zha_pages_device(handle)) if d is None else d
 
 
 def zha_pages_set_wait_limit(handle, cycles: int) -> None:
@@ -531,20 +543,43 @@ def _rows(d: zha_pages_desc, n: int, K: torch.Tensor, V: torch.Tensor, what: str
     return K.shape[2]
 
 
-def _here(handle, *tensors) -> None:
-    """Refuse tensors of another device than the cache's: its kernels run on that one."""
+def _on(handle, *tensors):
+    """Device addresses of contiguous tensors on the cache's device (None: a null pointer)."""
     dev = zha_pages_device(handle)
+    out = []
     for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != dev:
-            raise ValueError(f"tensor on {t.device}, the cache is on cuda:{dev}")
+        if t is None:
+            out.append(None)
+            continue
+        at = t.get_device()
+        if at != dev:
+            raise ValueError("libzha takes device tensors" if at < 0 else f"tensor on {t.device}, the cache is on cuda:{dev}")
+        if not t.is_contiguous():
+            raise ValueError("libzha takes contiguous tensors")
+        out.append(t.data_ptr())
+    return out
+
+
+def _raw_stream(handle, stream) -> int:
+    """The cudaStream_t of `stream` (None: the current one of the cache's device)."""
+    if stream is None:
+        return _current_raw_stream(zha_pages_device(handle))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _current_raw_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the same number without a Stream object
+    _current_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def zha_pages_load(handle, table: torch.Tensor, lens: torch.Tensor, stream=None) -> None:
     d = zha_pages_get_desc(handle)
     _expect(table, "table", d.max_seqs * d.max_seq_pages, _I32)
     _expect(lens, "lens", d.max_seqs, _I32)
-    _here(handle, table, lens)
-    _check(lib().zha_pages_load(handle, _ptr(table), _ptr(lens), _stream(stream)), "zha_pages_load")
+    _check(lib().zha_pages_load(handle, *_on(handle, table, lens), _raw_stream(handle, stream)), "zha_pages_load")
 
 
 def zha_pages_append(handle, K: torch.Tensor, V: torch.Tensor, seqs: torch.Tensor, K_new: torch.Tensor,
@@ -556,9 +591,8 @@ def zha_pages_append(handle, K: torch.Tensor, V: torch.Tensor, seqs: torch.Tenso
     n = _slots(seqs, "seqs")
     T = _rows(d, n, K_new, V_new, "_new")
     _expect(counts, "counts", n, _I32)
-    _here(handle, K, V, seqs, K_new, V_new, counts)
-    _check(lib().zha_pages_append(handle, _ptr(K), _ptr(V), _ptr(seqs), n, _ptr(K_new), _ptr(V_new), T,
-                                  _ptr(counts), _stream(stream)), "zha_pages_append")
+    k, v, s, kn, vn, c = _on(handle, K, V, seqs, K_new, V_new, counts)
+    _check(lib().zha_pages_append(handle, k, v, s, n, kn, vn, T, c, _raw_stream(handle, stream)), "zha_pages_append")
 
 
 def zha_pages_fork(handle, K: torch.Tensor, V: torch.Tensor, src: torch.Tensor, dst: torch.Tensor,
@@ -567,8 +601,7 @@ def zha_pages_fork(handle, K: torch.Tensor, V: torch.Tensor, src: torch.Tensor, 
     _pools(zha_pages_get_desc(handle), K, V)
     n = _slots(src, "src")
     _slots(dst, "dst", n)
-    _here(handle, K, V, src, dst)
-    _check(lib().zha_pages_fork(handle, _ptr(K), _ptr(V), _ptr(src), _ptr(dst), n, _stream(stream)),
+    _check(lib().zha_pages_fork(handle, *_on(handle, K, V, src, dst), n, _raw_stream(handle, stream)),
            "zha_pages_fork")
 
 
@@ -579,15 +612,14 @@ def zha_pages_copy(from_handle, K_from: torch.Tensor, V_from: torch.Tensor, hand
     _pools(zha_pages_get_desc(handle), K, V)
     n = _slots(src, "src")
     _slots(dst, "dst", n)
-    _here(handle, K_from, V_from, K, V, src, dst)
-    _check(lib().zha_pages_copy(from_handle, _ptr(K_from), _ptr(V_from), handle, _ptr(K), _ptr(V), _ptr(src),
-                                _ptr(dst), n, _stream(stream)), "zha_pages_copy")
+    kf, vf, k, v, a, b = _on(handle, K_from, V_from, K, V, src, dst)
+    _check(lib().zha_pages_copy(from_handle, kf, vf, handle, k, v, a, b, n, _raw_stream(handle, stream)),
+           "zha_pages_copy")
 
 
 def zha_pages_free(handle, seqs: torch.Tensor, stream=None) -> None:
     n = _slots(seqs, "seqs")
-    _here(handle, seqs)
-    _check(lib().zha_pages_free(handle, _ptr(seqs), n, _stream(stream)), "zha_pages_free")
+    _check(lib().zha_pages_free(handle, *_on(handle, seqs), n, _raw_stream(handle, stream)), "zha_pages_free")
 
 
 def zha_pages_compact(handle, K: torch.Tensor, V: torch.Tensor, live: torch.Tensor | None = None,
@@ -595,8 +627,7 @@ def zha_pages_compact(handle, K: torch.Tensor, V: torch.Tensor, live: torch.Tens
     """Move the pages in use to the bottom of the pools; live [1] receives how many there are."""
     _pools(zha_pages_get_desc(handle), K, V)
     _expect(live, "live", 1, _I32)
-    _here(handle, K, V, live)
-    _check(lib().zha_pages_compact(handle, _ptr(K), _ptr(V), _ptr(live), _stream(stream)), "zha_pages_compact")
+    _check(lib().zha_pages_compact(handle, *_on(handle, K, V, live), _raw_stream(handle, stream)), "zha_pages_compact")
 
 
 def zha_pages_gather(handle, K: torch.Tensor, V: torch.Tensor, seqs: torch.Tensor, K_out: torch.Tensor,
@@ -606,13 +637,12 @@ def zha_pages_gather(handle, K: torch.Tensor, V: torch.Tensor, seqs: torch.Tenso
     _pools(d, K, V)
     n = _slots(seqs, "seqs")
     cap = _rows(d, n, K_out, V_out, "_out")
-    _here(handle, K, V, seqs, K_out, V_out)
-    _check(lib().zha_pages_gather(handle, _ptr(K), _ptr(V), _ptr(seqs), n, _ptr(K_out), _ptr(V_out), cap,
-                                  _stream(stream)), "zha_pages_gather")
+    k, v, s, ko, vo = _on(handle, K, V, seqs, K_out, V_out)
+    _check(lib().zha_pages_gather(handle, k, v, s, n, ko, vo, cap, _raw_stream(handle, stream)), "zha_pages_gather")
 
 
 def zha_pages_check(handle, stream=None) -> int:
-    return int(lib().zha_pages_check(handle, _stream(stream)))
+    return int(lib().zha_pages_check(handle, _raw_stream(handle, stream)))
 
 
 def zha_prefix_attn_scratch_bytes(handle, batch: int, q_heads: int, nq: int, prefix_tokens: int) -> int:
@@ -631,11 +661,10 @@ def zha_prefix_attn_decode(handle, Q: torch.Tensor, K: torch.Tensor, V: torch.Te
     _expect(O, "O", Q.numel(), _OUT)
     _pools(d, K, V)
     _slots(seqs, "seqs", B)
-    _here(handle, Q, K, V, seqs, O, scratch)
-    _check(lib().zha_prefix_attn_decode(handle, _ptr(Q), dtype_code(Q.dtype), B, Hq, nq, _ptr(K), _ptr(V),
-                                        _ptr(seqs), prefix_seq, prefix_tokens, int(causal), scale, _ptr(O),
-                                        dtype_code(O.dtype), _ptr(scratch),
-                                        scratch.numel() * scratch.element_size(), _stream(stream)),
+    q, k, v, s, o, x = _on(handle, Q, K, V, seqs, O, scratch)
+    _check(lib().zha_prefix_attn_decode(handle, q, dtype_code(Q.dtype), B, Hq, nq, k, v, s, prefix_seq, prefix_tokens,
+                                        int(causal), scale, o, dtype_code(O.dtype), x,
+                                        scratch.numel() * scratch.element_size(), _raw_stream(handle, stream)),
            "zha_prefix_attn_decode")
 
 
