@@ -20,9 +20,9 @@ def _desc(**kw):
 
 
 def test_workspace_size():
-    # a 64-word header, five arrays of max_seqs, three of num_pages, the bitmap and the table
-    assert zha.zha_pages_workspace_bytes(_desc()) == 256 * (1 + 5 + 3 + 1 + 1)
-    assert zha.zha_pages_workspace_bytes(_desc(max_seqs=100, max_seq_pages=1000)) == 256 + 5 * 512 + 4 * 256 + 400128
+    # a 64-word header, eight arrays of max_seqs, five of num_pages, the bitmap and the table
+    assert zha.zha_pages_workspace_bytes(_desc()) == 256 * (1 + 8 + 4 + 1 + 1)
+    assert zha.zha_pages_workspace_bytes(_desc(max_seqs=100, max_seq_pages=1000)) == 256 + 8 * 512 + 5 * 256 + 400128
 
 
 @pytest.mark.parametrize("bad,status", [

@@ -11,9 +11,10 @@
 // A page that is only partly filled always belongs to one sequence (a fork copies it), so
 // appending never has to look whether somebody else reads the page.
 //
-// Calls that hand out pages are two launches: a plan (one CTA checks the list, finds the
-// pages, and either commits all of the call's bookkeeping or none of it) and the row kernel.  The
-// second starts while the first drains (programmatic launch).
+// Calls that hand out pages have two steps: a plan (one CTA checks the list, finds the
+// pages, and either commits all of the call's bookkeeping or none of it) and the rows.  In a small call
+// that CTA goes on with the rows; a large one is two launches, the second of which starts while the
+// first drains (programmatic launch).
 #include <cstdint>
 #include <cstdlib>
 
@@ -29,6 +30,27 @@ enum PlanMode { kAppend = 0, kFork = 1, kCopy = 2 };
 constexpr int kPlanThreads = 1024;
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kGroups = kPlanThreads / kRowThreads;  // groups of kRowThreads threads in the plan's CTA
+// Bytes that a small call moves at most.  A CTA moves 64 KB in about the 1.5 us of GPU time, and 2.5 us of the host's,
+// that a second launch costs (a cluster of eight CTAs as one launch took as long as the two launches).
+constexpr long long kSmallBytes = 64 * 1024;
+
+// Table entries that a free goes through entry by entry at most (one launch); above, by columns (two).
+constexpr long long kFewPages = 32 * 1024;
+
+// A group of kRowThreads threads: the x-th of nx that share some work.
+struct Group {
+  int x, nx, tid;
+  __device__ __forceinline__ int thread() const { return x * kRowThreads + tid; }
+  __device__ __forceinline__ int threads() const { return nx * kRowThreads; }
+  __device__ __forceinline__ int warp() const { return x * kRowWarps + (tid >> 5); }
+  __device__ __forceinline__ int warps() const { return nx * kRowWarps; }
+  __device__ static Group of_grid() { return {(int)blockIdx.x, (int)gridDim.x, (int)threadIdx.x}; }
+  // In a small call: this thread's group among the CTA's.
+  __device__ static Group of_cta() {
+    return {(int)(threadIdx.x / kRowThreads), kGroups, (int)(threadIdx.x % kRowThreads)};
+  }
+};
 
 __device__ __forceinline__ int ceil_shift(int x, int shift) { return (int)(((unsigned)x + (1u << shift) - 1u) >> shift); }
 
@@ -90,27 +112,34 @@ __device__ unsigned plan_entry(const PagesView& d, const PagesView& s, const int
   return 0;
 }
 
-// Bound: latency of a few dependent loads and two scans, about 4 us for any list of up to
-// 1,024 entries (one round); pages are found 32,768 at a time.
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(PagesView d, PagesView s, const int* src, const int* dst,
-                                                            const int* counts, int n, int T, int mode) {
+// The plan of a call, by one CTA of kPlanThreads threads.  Bound: latency of a few dependent loads and two
+// scans for any list of up to 1,024 entries (one round); pages are found 32,768 at a time.
+__device__ void plan_body(const PagesView& d, const PagesView& s, const int* src, const int* dst, const int* counts, int n,
+                          int T, int mode) {
   __shared__ int sums[32];
   __shared__ long long wide_sums[32];
   __shared__ unsigned bad;
   const int tid = threadIdx.x;
   if (tid == 0) bad = 0;
-  pdl_wait();
-  pdl_release();
+  // (used below; loaded with the lists)
+  const int free_pages = *d.free_pages;
+  unsigned word = tid < d.words ? d.used[tid] : ~0u;
   __syncthreads();
   long long total = 0;  // 64 bits: a list may ask for more pages than 31 bits count
+  int slot = -1, len = 0, cnt = 0;  // of the last round's entry
   // what each entry needs, and which entry names a slot first
   for (int at = 0; at < n; at += kPlanThreads) {
     const int i = at + tid;
-    int slot = -1, len = 0, cnt = 0, need = 0;
+    int need = 0;
+    slot = -1;
     if (i < n) {
       const unsigned e = plan_entry(d, s, src, dst, counts, T, mode, i, &slot, &len, &cnt, &need);
       if (e) atomicOr(&bad, e);
       if (slot >= 0) atomicMin(&d.claim[slot], i);
+      if (mode == kFork && (unsigned)src[i] < (unsigned)s.max_seqs) {
+        atomicAdd(&d.mult[src[i]], 1);
+        atomicMin(&d.lead[src[i]], i);
+      }
     }
     long long sum;
     const long long base = cta_scan<long long>(need, wide_sums, &sum);
@@ -122,27 +151,41 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PagesView d, PagesVi
     total += sum;
   }
   __syncthreads();
+  const bool one_round = n <= kPlanThreads;
   for (int i = tid; i < n; i += kPlanThreads) {
-    const int slot = dst[i];
-    if ((unsigned)slot < (unsigned)d.max_seqs && d.claim[slot] != i) atomicOr(&bad, kDevErrBadSeq);
+    const int x = one_round ? slot : dst[i];
+    if ((unsigned)x < (unsigned)d.max_seqs && __ldcg(&d.claim[x]) != i) atomicOr(&bad, kDevErrBadSeq);
   }
-  __syncthreads();
-  for (int i = tid; i < n; i += kPlanThreads) {
-    const int slot = dst[i];
-    if ((unsigned)slot < (unsigned)d.max_seqs) d.claim[slot] = kNoClaim;
-  }
-  if (tid == 0 && total > *d.free_pages) bad |= kDevErrPool;
-  __syncthreads();
-  if (bad) {
-    if (tid == 0) {
-      atomicOr(d.err, bad);
-      *d.ok = 0;
+  if (tid == 0 && total > free_pages) atomicOr(&bad, kDevErrPool);
+  if (mode == kFork)
+    for (int i = tid; i < n; i += kPlanThreads) {
+      const int from = src[i];
+      const bool first = (unsigned)from < (unsigned)s.max_seqs && __ldcg(&d.lead[from]) == i;
+      d.plan_mult[i] = first ? __ldcg(&d.mult[from]) : 0;
     }
-    return;
+  __syncthreads();
+  if (mode == kFork)
+    for (int i = tid; i < n; i += kPlanThreads) {
+      const int from = src[i];
+      if ((unsigned)from >= (unsigned)s.max_seqs) continue;
+      d.mult[from] = 0;
+      d.lead[from] = kNoClaim;
+    }
+  const unsigned error = bad;
+  for (int i = tid; i < n; i += kPlanThreads) {
+    const int x = one_round ? slot : dst[i];
+    if ((unsigned)x >= (unsigned)d.max_seqs) continue;
+    d.claim[x] = kNoClaim;
+    if (!error) d.lens[x] = one_round ? len + cnt : d.plan_len[i] + d.plan_cnt[i];
   }
+  if (tid == 0) {
+    if (error) atomicOr(d.err, error);
+    *d.ok = !error;
+    if (!error && total) *d.free_pages = free_pages - (int)total;
+  }
+  if (error) return;
   // the lowest free pages
   int given = 0;
-  unsigned word = tid < d.words ? d.used[tid] : ~0u;
   for (int at = 0; given < total && at < d.words; at += kPlanThreads) {
     const int w = at + tid;
     const unsigned next = w + kPlanThreads < d.words ? d.used[w + kPlanThreads] : ~0u;
@@ -162,11 +205,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PagesView d, PagesVi
     given += sum;
     word = next;
   }
-  for (int i = tid; i < n; i += kPlanThreads) d.lens[dst[i]] = d.plan_len[i] + d.plan_cnt[i];
-  if (tid == 0) {
-    *d.free_pages -= (int)total;
-    *d.ok = 1;
-  }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(PagesView d, PagesView s, const int* src, const int* dst,
+                                                            const int* counts, int n, int T, int mode) {
+  pdl_wait();
+  pdl_release();
+  plan_body(d, s, src, dst, counts, n, T, mode);
 }
 
 // ---------------------------------------------------------------- rows
@@ -198,28 +243,24 @@ __device__ __forceinline__ size_t page_vec(const PagesView& v, int page, int hea
   return ((size_t)page * v.heads + head) * ((size_t)v.page * v.row_vecs);
 }
 
-// blockIdx.y: list entry.  Rows of the entry's new tokens go to their pages; the entry's new
-// pages enter its table row.  A lane group of row_vecs lanes moves one row of K and of V.
-__global__ void __launch_bounds__(kRowThreads) append_kernel(PagesView d, const int* dst, int T, const uint4* Kn,
-                                                             const uint4* Vn, uint4* K, uint4* V) {
-  pdl_wait();
-  pdl_release();
-  if (!*d.ok) return;
-  const int i = blockIdx.y;
+// Rows of entry i's new tokens go to their pages; the entry's new pages enter its table row.  A lane group of
+// row_vecs lanes moves one row of K and of V.
+__device__ __forceinline__ void append_rows(const PagesView& d, int i, const Group& g, const int* dst, int T, const uint4* Kn,
+                                            const uint4* Vn, uint4* K, uint4* V) {
   const int slot = dst[i], len = d.plan_len[i], cnt = d.plan_cnt[i], base = d.plan_base[i];
   const int old = ceil_shift(len, d.shift), more = ceil_shift(len + cnt, d.shift) - old;
   int* row = d.table + (size_t)slot * d.width;
-  for (int j = blockIdx.x * kRowThreads + threadIdx.x; j < more; j += gridDim.x * kRowThreads) row[old + j] = d.fresh[base + j];
-  const int vecs = d.row_vecs, group = kRowThreads / vecs;  // rows per pass of the CTA
-  const int col = threadIdx.x % vecs, lane_row = threadIdx.x / vecs;
+  for (int j = g.thread(); j < more; j += g.threads()) row[old + j] = d.fresh[base + j];
+  const int vecs = d.row_vecs, at_once = kRowThreads / vecs;  // rows per pass of the group
+  const int col = g.tid % vecs, lane_row = g.tid / vecs;
   const unsigned rows = (unsigned)d.heads * (unsigned)cnt;
   constexpr int U = 4;
-  for (unsigned r0 = blockIdx.x * (group * U); r0 < rows; r0 += gridDim.x * (group * U)) {
+  for (unsigned r0 = g.x * (at_once * U); r0 < rows; r0 += g.nx * (at_once * U)) {
     uint4 a[U], b[U];
     size_t to[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const unsigned r = r0 + u * group + lane_row;
+      const unsigned r = r0 + u * at_once + lane_row;
       to[u] = ~(size_t)0;
       if (r < rows) {
         const unsigned h = r / (unsigned)cnt, t = r - h * cnt;
@@ -241,55 +282,89 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(PagesView d, const 
   }
 }
 
-// blockIdx.y: list entry.  Full pages are shared, a partial last page gets the entry's new page and its
-// rows copied.
-__global__ void __launch_bounds__(kRowThreads) fork_kernel(PagesView d, const int* src, const int* dst, uint4* K, uint4* V) {
-  pdl_wait();
-  pdl_release();
-  if (!*d.ok) return;
-  const int i = blockIdx.y;
-  const int len = d.plan_len[i], full = len >> d.shift, rest = len & (d.page - 1);
+// Entry i shares the source's full pages; a partial last page gets the entry's new page and its rows copied.
+// A page's count grows once for all the entries of its source.
+__device__ __forceinline__ void fork_rows(const PagesView& d, int i, const Group& g, const int* src, const int* dst, uint4* K,
+                                          uint4* V) {
+  const int len = d.plan_len[i], full = len >> d.shift, rest = len & (d.page - 1), forks = d.plan_mult[i];
   const int* from = d.table + (size_t)src[i] * d.width;
   int* row = d.table + (size_t)dst[i] * d.width;
-  for (int j = blockIdx.x * kRowThreads + threadIdx.x; j < full; j += gridDim.x * kRowThreads) {
+  for (int j = g.thread(); j < full; j += g.threads()) {
     const int page = from[j];
     row[j] = page;
-    if ((unsigned)page < (unsigned)d.num_pages) atomicAdd(&d.refs[page], 1);
+    if (forks && (unsigned)page < (unsigned)d.num_pages) atomicAdd(&d.refs[page], forks);
   }
   if (rest) {
     const int a = from[full], b = d.fresh[d.plan_base[i]];
-    if (blockIdx.x == 0 && threadIdx.x == 0) row[full] = b;
+    if (g.thread() == 0) row[full] = b;
     if ((unsigned)a >= (unsigned)d.num_pages) return;
-    const int lane = threadIdx.x & 31;
-    for (int h = blockIdx.x * kRowWarps + (threadIdx.x >> 5); h < d.heads; h += gridDim.x * kRowWarps) {
+    for (int h = g.warp(); h < d.heads; h += g.warps()) {
       const size_t x = page_vec(d, a, h), y = page_vec(d, b, h);
-      warp_copy(K + x, V + x, K + y, V + y, rest * d.row_vecs, lane);
+      warp_copy(K + x, V + x, K + y, V + y, rest * d.row_vecs, g.tid & 31);
     }
   }
 }
 
-// blockIdx.y: list entry.  Every page of the source is copied into a new one (rows past the
-// length are left alone); a warp takes one (page, head) at a time.
-__global__ void __launch_bounds__(kRowThreads) copy_kernel(PagesView d, PagesView s, const int* src, const int* dst,
-                                                           const uint4* Ks, const uint4* Vs, uint4* K, uint4* V) {
-  pdl_wait();
-  pdl_release();
-  if (!*d.ok) return;
-  const int i = blockIdx.y;
+// Every page of entry i's source is copied into a new one (rows past the length are left alone); a warp takes
+// one (page, head) at a time.
+__device__ __forceinline__ void copy_rows(const PagesView& d, const PagesView& s, int i, const Group& g, const int* src,
+                                          const int* dst, const uint4* Ks, const uint4* Vs, uint4* K, uint4* V) {
   const int len = d.plan_len[i], pages = ceil_shift(len, d.shift);
   const int* from = s.table + (size_t)src[i] * s.width;
   const int* fresh = d.fresh + d.plan_base[i];
   int* row = d.table + (size_t)dst[i] * d.width;
-  for (int j = blockIdx.x * kRowThreads + threadIdx.x; j < pages; j += gridDim.x * kRowThreads) row[j] = fresh[j];
-  const int lane = threadIdx.x & 31;
+  for (int j = g.thread(); j < pages; j += g.threads()) row[j] = fresh[j];
   const long long items = (long long)pages * d.heads;
-  for (long long x = blockIdx.x * kRowWarps + (threadIdx.x >> 5); x < items; x += (long long)gridDim.x * kRowWarps) {
+  for (long long x = g.warp(); x < items; x += g.warps()) {
     const int j = (int)(x / d.heads), h = (int)(x - (long long)j * d.heads);
     const int a = from[j], b = fresh[j];
     if ((unsigned)a >= (unsigned)s.num_pages) continue;
     const size_t p = page_vec(s, a, h), q = page_vec(d, b, h);
-    warp_copy(Ks + p, Vs + p, K + q, V + q, min(d.page, len - (j << d.shift)) * d.row_vecs, lane);
+    warp_copy(Ks + p, Vs + p, K + q, V + q, min(d.page, len - (j << d.shift)) * d.row_vecs, g.tid & 31);
   }
+}
+
+struct RowArgs {
+  PagesView d, s;       // the cache, and the one copied from
+  const int *src, *dst, *counts;
+  int n, T;
+  const uint4 *Kfrom, *Vfrom;  // new tokens, or the pools copied from
+  uint4 *K, *V;
+};
+
+template <int MODE>
+__device__ __forceinline__ void entry_rows(const RowArgs& x, int i, const Group& g) {
+  if constexpr (MODE == kAppend)
+    append_rows(x.d, i, g, x.dst, x.T, x.Kfrom, x.Vfrom, x.K, x.V);
+  else if constexpr (MODE == kFork)
+    fork_rows(x.d, i, g, x.src, x.dst, x.K, x.V);
+  else
+    copy_rows(x.d, x.s, i, g, x.src, x.dst, x.Kfrom, x.Vfrom, x.K, x.V);
+}
+
+// blockIdx.y: list entry.
+template <int MODE>
+__global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ RowArgs x) {
+  pdl_wait();
+  pdl_release();
+  if (!*x.d.ok) return;
+  entry_rows<MODE>(x, blockIdx.y, Group::of_grid());
+}
+
+// Plan and rows of a small call, one CTA.
+template <int MODE>
+__global__ void __launch_bounds__(kPlanThreads) small_kernel(const __grid_constant__ RowArgs x) {
+  pdl_wait();
+  pdl_release();
+  plan_body(x.d, x.s, x.src, x.dst, x.counts, x.n, x.T, MODE);
+  __syncthreads();
+  if (!*x.d.ok) return;
+  Group g = Group::of_cta();
+  const int each = max(1, kGroups / x.n), sets = kGroups / each, set = g.x / each;  // each: groups per entry
+  g.x %= each;
+  g.nx = each;
+  if (set < sets)
+    for (int i = set; i < x.n; i += sets) entry_rows<MODE>(x, i, g);
 }
 
 // blockIdx.y: list entry.  Rows [0, len) of the sequence to the dense cache.
@@ -321,9 +396,9 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(PagesView s, const 
   }
 }
 
-// One CTA per list entry.  Whoever takes the length away frees the sequence, so a slot that is
+// One CTA per list entry (few pages in all).  Whoever takes the length away frees the sequence, so a slot that is
 // named twice is freed once.
-__global__ void __launch_bounds__(kPlanThreads) free_kernel(PagesView d, const int* seqs) {
+__global__ void __launch_bounds__(kRowThreads) free_kernel(PagesView d, const int* seqs) {
   __shared__ int s_len, s_freed;
   pdl_wait();
   pdl_release();
@@ -340,7 +415,7 @@ __global__ void __launch_bounds__(kPlanThreads) free_kernel(PagesView d, const i
   const int pages = ceil_shift(s_len, d.shift);
   int* row = d.table + (size_t)slot * d.width;
   int freed = 0;
-  for (int j = threadIdx.x; j < pages; j += kPlanThreads) {
+  for (int j = threadIdx.x; j < pages; j += kRowThreads) {
     const int page = row[j];
     row[j] = -1;
     if ((unsigned)page < (unsigned)d.num_pages && atomicSub(&d.refs[page], 1) == 1) {
@@ -352,6 +427,103 @@ __global__ void __launch_bounds__(kPlanThreads) free_kernel(PagesView d, const i
   if ((threadIdx.x & 31) == 0 && freed) atomicAdd(&s_freed, freed);
   __syncthreads();
   if (threadIdx.x == 0 && s_freed) atomicAdd(d.free_pages, s_freed);
+}
+
+// Many pages: the lengths first, by one CTA, into plan_len (0 for a slot that a lower entry names too) ..
+__global__ void __launch_bounds__(kPlanThreads) free_plan_kernel(PagesView d, const int* seqs, int n) {
+  pdl_wait();
+  pdl_release();
+  for (int i = threadIdx.x; i < n; i += kPlanThreads) {
+    const int slot = seqs[i];
+    if ((unsigned)slot < (unsigned)d.max_seqs)
+      atomicMin(&d.claim[slot], i);
+    else
+      atomicOr(d.err, kDevErrBadSeq);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kPlanThreads) {
+    const int slot = seqs[i];
+    d.plan_len[i] = (unsigned)slot < (unsigned)d.max_seqs && __ldcg(&d.claim[slot]) == i ? d.lens[slot] : 0;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kPlanThreads) {
+    const int slot = seqs[i];
+    if ((unsigned)slot >= (unsigned)d.max_seqs) continue;
+    d.claim[slot] = kNoClaim;
+    d.lens[slot] = 0;
+  }
+}
+
+// .. then the table by columns: a thread takes a column of kRun entries.  Forks hold the same page in the same column,
+// so a run of equal pages changes its count once (63 forks of 8,192 pages: 5 us; page by page 41 us,
+// half a million counts to 8,192 places).
+constexpr int kRun = 16;
+
+struct Columns {
+  const int* row[kRun];  // table rows, null: none
+  int pages[kRun], most;
+};
+
+// Fills *c (shared memory) with entries first .. of n: slot and tokens by `get(i, &slot, &len)`.
+template <typename Get>
+__device__ __forceinline__ void columns_of(const PagesView& d, const int* table, int first, int n, Columns* c, Get get) {
+  const int i = threadIdx.x;
+  if (i < kRun) {
+    int slot = 0, len = 0;
+    if (first + i < n) get(first + i, &slot, &len);
+    c->pages[i] = ceil_shift(len, d.shift);
+    c->row[i] = table + (size_t)slot * d.width;
+  }
+  __syncthreads();
+  if (i == 0) {
+    int most = 0;
+    for (int k = 0; k < kRun; ++k) most = max(most, c->pages[k]);
+    c->most = most;
+  }
+  __syncthreads();
+}
+
+__global__ void __launch_bounds__(kRowThreads) free_columns_kernel(PagesView d, const int* seqs, int n) {
+  __shared__ Columns c;
+  pdl_wait();
+  pdl_release();
+  columns_of(d, d.table, blockIdx.y * kRun, n, &c, [&](int i, int* slot, int* len) {
+    *len = d.plan_len[i];
+    *slot = *len ? seqs[i] : 0;
+  });
+  int freed = 0;
+  for (int j = blockIdx.x * kRowThreads + threadIdx.x; j < c.most; j += gridDim.x * kRowThreads) {
+    int page[kRun];
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) page[k] = j < c.pages[k] ? c.row[k][j] : -1;
+#pragma unroll
+    for (int k = 0; k < kRun; ++k)
+      if (j < c.pages[k]) const_cast<int*>(c.row[k])[j] = -1;
+    int run = 0, less[kRun], held[kRun];  // by how much each run's count falls (at its last entry)
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+      less[k] = 0;
+      if ((unsigned)page[k] >= (unsigned)d.num_pages) continue;
+      ++run;
+      bool more = false;  // the same page again, no other between
+#pragma unroll
+      for (int x = kRun - 1; x > k; --x)
+        if (page[x] >= 0) more = page[x] == page[k];
+      if (more) continue;
+      less[k] = run;
+      run = 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) held[k] = less[k] ? atomicSub(&d.refs[page[k]], less[k]) : 0;
+#pragma unroll
+    for (int k = 0; k < kRun; ++k)
+      if (less[k] && held[k] == less[k]) {
+        atomicAnd(&d.used[page[k] >> 5], ~(1u << (page[k] & 31)));
+        ++freed;
+      }
+  }
+  freed = __reduce_add_sync(0xffffffffu, freed);
+  if ((threadIdx.x & 31) == 0 && freed) atomicAdd(d.free_pages, freed);
 }
 
 // ---------------------------------------------------------------- compact
@@ -428,10 +600,12 @@ __global__ void __launch_bounds__(kRowThreads) init_kernel(PagesView d) {
   pdl_wait();
   const size_t at = (size_t)blockIdx.x * kRowThreads + threadIdx.x, step = (size_t)gridDim.x * kRowThreads;
   for (size_t i = at; i < (size_t)d.max_seqs * d.width; i += step) d.table[i] = -1;
-  for (size_t i = at; i < (size_t)d.num_pages; i += step) d.refs[i] = 0;
+  for (size_t i = at; i < (size_t)d.num_pages; i += step) {
+    d.refs[i] = d.count[i] = d.partial[i] = 0;
+  }
   for (size_t i = at; i < (size_t)d.max_seqs; i += step) {
-    d.lens[i] = 0;
-    d.claim[i] = kNoClaim;
+    d.lens[i] = d.mult[i] = 0;
+    d.claim[i] = d.lead[i] = kNoClaim;
   }
   for (size_t i = at; i < (size_t)d.words; i += step) {
     const long long left = (long long)d.num_pages - 32 * (long long)i;
@@ -443,80 +617,108 @@ __global__ void __launch_bounds__(kRowThreads) init_kernel(PagesView d) {
     *d.free_pages = d.num_pages;
     *d.moves = 0;
     *d.live = 0;
+    *d.load_bad = *d.ticket = 0;
   }
 }
 
-__global__ void __launch_bounds__(kRowThreads) load_clear_kernel(PagesView d) {
-  pdl_wait();
-  pdl_release();
-  for (int i = blockIdx.x * kRowThreads + threadIdx.x; i < d.num_pages; i += gridDim.x * kRowThreads) {
-    d.name[i] = 0;
-    d.fresh[i] = 0;
-  }
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    *d.ok = 1;
-    *d.free_pages = d.num_pages;
-  }
-}
-
-// blockIdx.x: slot.  Counts the pages' holders into `name`; `fresh` marks partial last pages.
+// Counts the pages' holders, by columns of kRun slots as above, and marks partly filled last pages.
 __global__ void __launch_bounds__(kRowThreads) load_count_kernel(PagesView d, const int* table, const int* lens) {
+  __shared__ Columns c;
+  __shared__ int partial[kRun];  // the column of a slot's partial last page, or -1
   pdl_wait();
   pdl_release();
-  const int s = blockIdx.x, len = lens[s];
-  if (len < 0 || (long long)len > (long long)d.width << d.shift) {
-    if (threadIdx.x == 0) *d.ok = 0;
-    return;
-  }
-  const int pages = ceil_shift(len, d.shift);
-  const bool rest = (len & (d.page - 1)) != 0;
-  for (int j = threadIdx.x; j < pages; j += kRowThreads) {
-    const int page = table[(size_t)s * d.width + j];
-    if ((unsigned)page >= (unsigned)d.num_pages)
-      *d.ok = 0;
-    else {
-      atomicAdd(&d.name[page], 1);
-      if (rest && j == pages - 1) d.fresh[page] = 1;
+  columns_of(d, table, blockIdx.y * kRun, d.max_seqs, &c, [&](int i, int* slot, int* len) {
+    *slot = i;
+    *len = lens[i];
+    if (*len < 0 || (long long)*len > (long long)d.width << d.shift) {
+      *d.load_bad = 1;
+      *len = 0;
     }
+    partial[i % kRun] = *len & (d.page - 1) ? *len >> d.shift : -1;
+  });
+  for (int j = blockIdx.x * kRowThreads + threadIdx.x; j < c.most; j += gridDim.x * kRowThreads) {
+    int page[kRun];
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) page[k] = j < c.pages[k] ? c.row[k][j] : -1;
+    int run = 0;
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+      if (j >= c.pages[k]) continue;
+      if ((unsigned)page[k] >= (unsigned)d.num_pages) {
+        bad = true;
+        page[k] = -1;
+        continue;
+      }
+      ++run;
+      if (partial[k] == j) d.partial[page[k]] = 1;
+      bool more = false;
+#pragma unroll
+      for (int x = kRun - 1; x > k; --x)
+        if (page[x] >= 0) more = page[x] == page[k];
+      if (more) continue;
+      atomicAdd(&d.count[page[k]], run);
+      run = 0;
+    }
+    if (bad) *d.load_bad = 1;
   }
 }
 
+// A partly filled last page has one holder.
 __global__ void __launch_bounds__(kRowThreads) load_check_kernel(PagesView d) {
   pdl_wait();
   pdl_release();
-  for (int i = blockIdx.x * kRowThreads + threadIdx.x; i < d.num_pages; i += gridDim.x * kRowThreads)
-    if (d.fresh[i] && d.name[i] > 1) *d.ok = 0;
+  for (int i = blockIdx.x * kRowThreads + threadIdx.x; i < d.num_pages; i += gridDim.x * kRowThreads) {
+    if (d.partial[i] && d.count[i] > 1) *d.load_bad = 1;
+    d.partial[i] = 0;
+  }
 }
 
 // Adopts the counted table, or leaves an empty cache when something in it did not hold.
 __global__ void __launch_bounds__(kRowThreads) load_apply_kernel(PagesView d, const int* table, const int* lens) {
   pdl_wait();
   pdl_release();
-  const bool ok = *d.ok;
+  const bool ok = !*d.load_bad;
   for (int s = blockIdx.x; s < d.max_seqs; s += gridDim.x) {
+    // (table and lens may be the cache's own: every entry is read and written by one thread)
     const int len = ok ? lens[s] : 0, pages = ceil_shift(len, d.shift);
-    for (int j = threadIdx.x; j < d.width; j += kRowThreads)
-      d.table[(size_t)s * d.width + j] = j < pages ? table[(size_t)s * d.width + j] : -1;
-    __syncthreads();  // (lens may be the cache's own)
+    const size_t row = (size_t)s * d.width;
+    constexpr int U = 4;
+    for (int j0 = threadIdx.x; j0 < d.width; j0 += U * kRowThreads) {
+      int page[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) page[u] = j0 + u * kRowThreads < pages ? table[row + j0 + u * kRowThreads] : -1;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (j0 + u * kRowThreads < d.width) d.table[row + j0 + u * kRowThreads] = page[u];
+    }
+    __syncthreads();  // all have read the length
     if (threadIdx.x == 0) d.lens[s] = len;
   }
   // a warp makes one word of the bitmap
-  const int lane = threadIdx.x & 31;
-  for (int w = blockIdx.x * kRowWarps + (threadIdx.x >> 5); w < d.words; w += gridDim.x * kRowWarps) {
+  const Group g = Group::of_grid();
+  const int lane = g.tid & 31;
+  for (int w = g.warp(); w < d.words; w += g.warps()) {
     const int page = w * 32 + lane;
     int refs = 0;
     if (page < d.num_pages) {
-      refs = ok ? d.name[page] : 0;
+      refs = ok ? d.count[page] : 0;
+      d.count[page] = 0;
       d.refs[page] = refs;
     }
     const unsigned held = __ballot_sync(0xffffffffu, page >= d.num_pages || refs > 0);
-    const int n = __popc(__ballot_sync(0xffffffffu, page < d.num_pages && refs > 0));
     if (lane == 0) {
+      const int more = __popc(d.used[w]) - __popc(held);  // pages that become free
       d.used[w] = held;
-      if (n) atomicSub(d.free_pages, n);
+      if (more) atomicAdd(d.free_pages, more);
     }
   }
-  if (!ok && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(d.err, kDevErrBadSeq);
+  // the last CTA to leave (all have looked) puts the flag back
+  if (threadIdx.x == 0 && atomicAdd(d.ticket, 1) == (int)gridDim.x - 1) {
+    *d.ticket = 0;
+    *d.load_bad = 0;
+    if (!ok) atomicOr(d.err, kDevErrBadSeq);
+  }
 }
 
 // ---------------------------------------------------------------- host
@@ -554,6 +756,8 @@ size_t layout(const zha_pages_desc* d, char* base, PagesView* v) {
   v->free_pages = head + 2;
   v->moves = head + 3;
   v->live = head + 4;
+  v->load_bad = head + 5;
+  v->ticket = head + 6;
   v->max_seqs = d->max_seqs;
   v->width = d->max_seq_pages;
   v->num_pages = d->num_pages;
@@ -568,15 +772,42 @@ size_t layout(const zha_pages_desc* d, char* base, PagesView* v) {
   v->plan_len = take(d->max_seqs);
   v->plan_cnt = take(d->max_seqs);
   v->plan_base = take(d->max_seqs);
+  v->plan_mult = take(d->max_seqs);
+  v->mult = take(d->max_seqs);
+  v->lead = take(d->max_seqs);
   v->refs = take(d->num_pages);
   v->fresh = take(d->num_pages);
   v->name = take(d->num_pages);
+  v->count = take(d->num_pages);
+  v->partial = take(d->num_pages);
   v->used = reinterpret_cast<unsigned*>(take(v->words));
   v->table = take((size_t)d->max_seqs * d->max_seq_pages);
   return at;
 }
 
 zha_status cuda_status(cudaError_t e) { return e == cudaSuccess ? ZHA_OK : ZHA_ERR_CUDA; }
+
+// Plan and rows of a call that hands out pages and moves at most `bytes`.
+template <int MODE>
+zha_status launch_rows(zha_pages* p, const RowArgs& x, long long bytes, unsigned grid_x, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (bytes <= kSmallBytes) {
+    e = launch_pdl(small_kernel<MODE>, dim3(1), dim3(kPlanThreads), 0, s, x);
+    p->launches += 1;
+  } else {
+    e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, x.d, x.s, x.src, x.dst, x.counts, x.n, x.T, (int)MODE);
+    if (e == cudaSuccess) e = launch_pdl(rows_kernel<MODE>, dim3(grid_x, x.n), dim3(kRowThreads), 0, s, x);
+    p->launches += 2;
+  }
+  return cuda_status(e);
+}
+
+// CTAs over the columns of a table.
+unsigned column_grid(const zha_pages* p) {
+  const int g = (p->desc.max_seq_pages + kRowThreads - 1) / kRowThreads;
+  return (unsigned)(g < 2 * p->sms ? g : 2 * p->sms);
+}
 
 // CTAs over blockIdx.x so that `entries` list entries fill the device about eight CTAs deep,
 // and no more than `items` units of work per CTA could use.
@@ -645,12 +876,12 @@ zha_status zha_pages_load(zha_pages* p, const int* d_table, const int* d_lens, v
   if (!p || !d_table || !d_lens || !aligned(d_table, 4) || !aligned(d_lens, 4) || !on_device(p))
     return ZHA_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const dim3 block(kRowThreads), wide(2 * p->sms);
-  cudaError_t e = launch_pdl(load_clear_kernel, wide, block, 0, s, p->v);
-  if (e == cudaSuccess) e = launch_pdl(load_count_kernel, dim3(p->desc.max_seqs), block, 0, s, p->v, d_table, d_lens);
-  if (e == cudaSuccess) e = launch_pdl(load_check_kernel, wide, block, 0, s, p->v);
-  if (e == cudaSuccess) e = launch_pdl(load_apply_kernel, wide, block, 0, s, p->v, d_table, d_lens);
-  p->launches += 4;
+  const zha_pages_desc& d = p->desc;
+  const dim3 block(kRowThreads), columns(column_grid(p), (d.max_seqs + kRun - 1) / kRun);
+  cudaError_t e = launch_pdl(load_count_kernel, columns, block, 0, s, p->v, d_table, d_lens);
+  if (e == cudaSuccess) e = launch_pdl(load_check_kernel, dim3(p->sms), block, 0, s, p->v);
+  if (e == cudaSuccess) e = launch_pdl(load_apply_kernel, dim3(4 * p->sms), block, 0, s, p->v, d_table, d_lens);
+  p->launches += 3;
   return cuda_status(e);
 }
 
@@ -662,16 +893,11 @@ zha_status zha_pages_append(zha_pages* p, void* d_K, void* d_V, const int* d_seq
   if (skip || tokens == 0) return ZHA_OK;
   if (!vectors(d_K, d_V) || !vectors(d_Knew, d_Vnew) || !aligned(d_counts, 4)) return ZHA_ERR_INVALID_ARG;
   if (tokens > 1 << 30 || (long long)tokens * p->desc.kv_heads > 1LL << 30) return ZHA_ERR_UNSUPPORTED;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p->v, p->v, (const int*)nullptr, d_seqs,
-                             d_counts, n, tokens, (int)kAppend);
-  const int per_cta = kRowThreads / p->v.row_vecs * 4;
-  const dim3 grid(row_grid(p, n, (long long)tokens * p->desc.kv_heads, per_cta), n);
-  if (e == cudaSuccess)
-    e = launch_pdl(append_kernel, grid, dim3(kRowThreads), 0, s, p->v, d_seqs, tokens, (const uint4*)d_Knew,
-                   (const uint4*)d_Vnew, (uint4*)d_K, (uint4*)d_V);
-  p->launches += 2;
-  return cuda_status(e);
+  const RowArgs x = {p->v, p->v, nullptr, d_seqs, d_counts, n, tokens, (const uint4*)d_Knew, (const uint4*)d_Vnew,
+                     (uint4*)d_K, (uint4*)d_V};
+  const long long rows = (long long)tokens * p->desc.kv_heads;
+  return launch_rows<kAppend>(p, x, 32LL * n * rows * p->v.row_vecs,
+                              row_grid(p, n, rows, kRowThreads / p->v.row_vecs * 4), stream);
 }
 
 zha_status zha_pages_fork(zha_pages* p, void* d_K, void* d_V, const int* d_src, const int* d_dst, int n, void* stream) {
@@ -679,14 +905,10 @@ zha_status zha_pages_fork(zha_pages* p, void* d_K, void* d_V, const int* d_src, 
   const zha_status st = list_status(p, d_src, n, &skip);
   if (st != ZHA_OK || skip) return st;
   if (!d_dst || !aligned(d_dst, 4) || !vectors(d_K, d_V)) return ZHA_ERR_INVALID_ARG;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p->v, p->v, d_src, d_dst,
-                             (const int*)nullptr, n, 0, (int)kFork);
-  const dim3 grid(row_grid(p, n, p->desc.max_seq_pages, kRowThreads), n);
-  if (e == cudaSuccess)
-    e = launch_pdl(fork_kernel, grid, dim3(kRowThreads), 0, s, p->v, d_src, d_dst, (uint4*)d_K, (uint4*)d_V);
-  p->launches += 2;
-  return cuda_status(e);
+  const RowArgs x = {p->v, p->v, d_src, d_dst, nullptr, n, 0, nullptr, nullptr, (uint4*)d_K, (uint4*)d_V};
+  const long long tail = 32LL * p->v.page * p->v.heads * p->v.row_vecs;  // K and V of a page
+  return launch_rows<kFork>(p, x, n * (tail + 8LL * p->desc.max_seq_pages), row_grid(p, n, p->desc.max_seq_pages, kRowThreads),
+                            stream);
 }
 
 zha_status zha_pages_copy(const zha_pages* from, const void* d_Kfrom, const void* d_Vfrom, zha_pages* p, void* d_K,
@@ -700,24 +922,26 @@ zha_status zha_pages_copy(const zha_pages* from, const void* d_Kfrom, const void
     return ZHA_ERR_INVALID_ARG;
   if (skip) return ZHA_OK;
   if (!d_dst || !aligned(d_dst, 4) || !vectors(d_K, d_V) || !vectors(d_Kfrom, d_Vfrom)) return ZHA_ERR_INVALID_ARG;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p->v, from->v, d_src, d_dst,
-                             (const int*)nullptr, n, 0, (int)kCopy);
-  const dim3 grid(row_grid(p, n, (long long)p->desc.max_seq_pages * p->desc.kv_heads, kRowWarps), n);
-  if (e == cudaSuccess)
-    e = launch_pdl(copy_kernel, grid, dim3(kRowThreads), 0, s, p->v, from->v, d_src, d_dst, (const uint4*)d_Kfrom,
-                   (const uint4*)d_Vfrom, (uint4*)d_K, (uint4*)d_V);
-  p->launches += 2;
-  return cuda_status(e);
+  const RowArgs x = {p->v, from->v, d_src, d_dst, nullptr, n, 0, (const uint4*)d_Kfrom, (const uint4*)d_Vfrom, (uint4*)d_K,
+                     (uint4*)d_V};
+  const long long page = 32LL * p->v.page * p->v.heads * p->v.row_vecs;
+  return launch_rows<kCopy>(p, x, n * p->desc.max_seq_pages * page,
+                            row_grid(p, n, (long long)p->desc.max_seq_pages * p->desc.kv_heads, kRowWarps), stream);
 }
 
 zha_status zha_pages_free(zha_pages* p, const int* d_seqs, int n, void* stream) {
   bool skip;
   const zha_status st = list_status(p, d_seqs, n, &skip);
   if (st != ZHA_OK || skip) return st;
-  const cudaError_t e = launch_pdl(free_kernel, dim3(n), dim3(kPlanThreads), 0, static_cast<cudaStream_t>(stream),
-                                   p->v, d_seqs);
-  p->launches += 1;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((long long)n * p->desc.max_seq_pages <= kFewPages) {
+    p->launches += 1;
+    return cuda_status(launch_pdl(free_kernel, dim3(n), dim3(kRowThreads), 0, s, p->v, d_seqs));
+  }
+  cudaError_t e = launch_pdl(free_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p->v, d_seqs, n);
+  if (e == cudaSuccess)
+    e = launch_pdl(free_columns_kernel, dim3(column_grid(p), (n + kRun - 1) / kRun), dim3(kRowThreads), 0, s, p->v, d_seqs, n);
+  p->launches += 2;
   return cuda_status(e);
 }
 
