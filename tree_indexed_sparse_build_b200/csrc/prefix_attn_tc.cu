@@ -221,15 +221,14 @@ struct Loader {
     while (x.any) {
       const bool dual = x.dual();
       const int by = dual ? 1 : 2;
-      if (KEYS && x.t == x.g.t0)
-        for (int i = 0; i < 1 + dual; ++i)
-          if (!queries(x.g, x.g.tile + i)) return false;
+      const Segment g = x.g;
+      const bool with_queries = KEYS && x.t == x.g.t0;
       int flags = dual ? kPaired : 0;
       if (x.t < x.g.t0 + by) flags |= kFirst;
       if (x.t + by >= x.g.t1) flags |= kLast;
       if (KEYS) {
         if (dual || x.g.t1 - x.g.t0 == 1) flags |= kAlone;
-        flags |= ((qc - 1 - dual) & 3) * kQuery;
+        flags |= ((with_queries ? qc : qc - 1 - dual) & 3) * kQuery;
       }
       const int n = x.keys(a), y = x.k0(a) & (a.v.page - 1) & ~(args.chunk - 1), z = page * a.s.heads + x.g.head;
       const bool load = page >= 0;
@@ -247,6 +246,10 @@ struct Loader {
                   &full[at.stage]);
       at.add(1);
       ++tiles;
+      // the queries after the keys: they wait for the segment before the last, the keys need not
+      if (with_queries)
+        for (int i = 0; i < 1 + dual; ++i)
+          if (!queries(g, g.tile + i)) return false;
     }
     if (KEYS)
       for (int i = 0; i < 2; ++i) {  // where each stream's next tile would be
