@@ -421,8 +421,9 @@ const int* zha_pages_refs(const zha_pages* pages);
 long long zha_pages_launch_count(const zha_pages* pages);
 zha_status zha_pages_get_desc(const zha_pages* pages, zha_pages_desc* out);
 int zha_pages_device(const zha_pages* pages);
-/* As zha_tree_set_wait_limit: bounds the attention's first wait for its copies (0: default).  Outputs
- * of a call whose wait ran out are NaN. */
+/* As zha_tree_set_wait_limit: bounds the attention's waits for its copies (0: default).  When one runs out, the
+ * call returns with ZHA_ERR_TIMEOUT in the error word, and its outputs, and those of later calls until
+ * zha_pages_check has reported it, are NaN. */
 zha_status zha_pages_set_wait_limit(zha_pages* pages, long long cycles);
 
 const char* zha_status_string(zha_status status);

@@ -310,6 +310,121 @@ def test_pools_behind_two_to_the_31(kv):
     _compare(got, Q, ks, vs, small, lens, [0, 1], 0.1, 0, page, False, kv, kv, F32)
 
 
+@pytest.mark.parametrize("heads,group,d,page,prefix,lens,nq", [
+    (8, 4, 128, 64, 8192, [8192 + 1 + 37 * i for i in range(64)], 1),   # dual tiles, many own items of several lengths
+    (2, 8, 128, 16, 16384, [16384 + (i * 211) % 500 for i in range(16)], 1),  # one row tile, long runs of single tiles
+    (8, 4, 64, 32, 4096, [4096 + 129 * (i % 4) for i in range(300)], 1),
+    (1, 4, 128, 8, 0, [1 + (97 * i) % 4000 for i in range(70)], 3),
+    (4, 1, 64, 256, 512, [513 + i for i in range(200)], 1),
+    (3, 5, 128, 128, 2048, [2048 + 300 * i for i in range(9)], 11),
+])
+def test_long_pipelines_against_the_fp32_kernel(heads, group, d, page, prefix, lens, nq):
+    # many tiles per CTA on the tensor cores against the fp32 kernel on the same numbers (an fp32 query tensor
+    # of bf16 values), and the same bits in three calls
+    zha = _zha()
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    width = -(-max(lens) // page)
+    shared = prefix // page
+    num = shared + sum(-(-n // page) - shared for n in lens)
+    pages = zha.Pages(heads, d, page, num, len(lens), width, BF16)
+    K, V = (torch.randn((num, heads, page, d), generator=gen, device="cuda").to(BF16) for _ in "KV")
+    ids, at = torch.randperm(num, generator=gen, device="cuda").int(), shared
+    table = torch.full((len(lens), width), -1, dtype=torch.int32, device="cuda")
+    table[:, :shared] = ids[:shared]
+    for s, n in enumerate(lens):
+        k = -(-n // page) - shared
+        table[s, shared:shared + k] = ids[at:at + k]
+        at += k
+        if n % page and k > 0:  # rows without a token
+            K[ids[at - 1].long(), :, n % page:] = float("nan")
+            V[ids[at - 1].long(), :, n % page:] = float("inf")
+    pages.load(table, _i32(lens))
+    seqs = _i32(list(range(len(lens))))
+    Q = torch.randn((len(lens), heads * group, nq, d), generator=gen, device="cuda").to(BF16)
+    got = [pages.attend(Q, K, V, d ** -0.5, seqs, 0, prefix, nq > 1, F32) for _ in range(3)]
+    want = pages.attend(Q.float(), K, V, d ** -0.5, seqs, 0, prefix, nq > 1, F32).double()
+    assert pages.check() == zha.ZHA_OK
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+    # |scale q k| summed over d is below 6 sigma products' sum, (d + 3) 2^-22 of which is below 1e-3 of a weight's
+    # size; weights add 2^-16.  sum(p |v|) is at most max |v| < 6, outputs are about |v| / sqrt(n): compare by rows
+    bound = 2.0 ** -16 + 2 * (d + 3) * 2.0 ** -23 * d ** -0.5 * d * 4 + 2 * (max(lens) + 64) * 2.0 ** -23
+    assert ((got[0].double() - want).abs().amax(-1) <= bound * 6).all()
+    # and rounded to bf16 at the end: 2^-8 of sum(p |v|) (below E|v| + 6 sigma / sqrt(n) < 6) and of the output
+    bf = pages.attend(Q, K, V, d ** -0.5, seqs, 0, prefix, nq > 1).double()
+    assert ((bf - want).abs() <= (2.0 ** -8 + bound) * 6).all()
+
+
+def test_more_entries_than_slots():
+    zha = _zha()
+    for kv in (F32, BF16):
+        lens = [70, 90, 64]
+        pages, Q, K, V, table = _case(zha, 2, 2, 64, 16, 64, lens, 1, kv, kv)
+        q, k, v = Q.repeat(40, 1, 1, 1).cuda(), K.cuda(), V.cuda()
+        seqs = [0, 1, 2] * 40
+        got = pages.attend(q, k, v, 0.2, _i32(seqs), 0, 64, out_dtype=F32)
+        _compare(got, q.cpu(), K, V, table, lens, seqs, 0.2, 0, 64, False, kv, kv, F32)
+
+
+def test_output_in_the_place_of_the_queries():
+    zha = _zha()
+    for kv in (F32, BF16):
+        lens = [300, 640, 257]
+        pages, Q, K, V, table = _case(zha, 2, 2, 64, 16, 256, lens, 2, kv, kv)
+        q = Q.cuda()
+        got = pages.attend(q, K.cuda(), V.cuda(), 0.2, _i32([0, 1, 2]), 0, 256, True, O=q)
+        assert got is q
+        _compare(q, Q, K, V, table, lens, [0, 1, 2], 0.2, 0, 256, True, kv, kv, kv)
+
+
+def test_refusals_with_a_cache():
+    zha = _zha()
+    pages, Q, K, V, table = _case(zha, 2, 2, 64, 16, 32, [40, 50], 1, F32, F32)
+    q, k, v, s = Q.cuda(), K.cuda(), V.cuda(), _i32([0, 1])
+    for status, call in [
+        (zha.ZHA_ERR_INVALID_ARG, lambda: pages.attend(q, k, v, float("nan"), s)),
+        (zha.ZHA_ERR_INVALID_ARG, lambda: pages.attend(q, k, v, float("inf"), s)),
+        (zha.ZHA_ERR_INVALID_ARG, lambda: pages.attend(q[:, :3].contiguous(), k, v, 0.1, s)),  # 3 heads over 2
+        (zha.ZHA_ERR_INVALID_ARG, lambda: pages.attend(q, k, v, 0.1, s, prefix_tokens=24)),    # inside a page
+        (zha.ZHA_ERR_INVALID_ARG, lambda: pages.attend(q, k, v, 0.1, s, prefix_tokens=-16)),
+        (zha.ZHA_ERR_INVALID_ARG, lambda: pages.attend(q, k, v, 0.1, s, prefix_seq=2, prefix_tokens=16)),
+        (zha.ZHA_ERR_CAPACITY, lambda: pages.attend(q, k, v, 0.1, s, prefix_tokens=16 * 100)),
+        (zha.ZHA_ERR_INVALID_ARG, lambda: pages.free(_i32([0, 1, 0]))),                         # more than slots
+        (zha.ZHA_ERR_INVALID_ARG, lambda: zha.zha_prefix_attn_decode(
+            pages.handle, q, k, v, s, 0, 32, False, 0.1, q.clone(), torch.zeros(64, device="cuda"))),  # scratch
+    ]:
+        with pytest.raises(zha.ZhaError) as e:
+            call()
+        assert e.value.status == status
+    for what, call in [
+        ("contiguous", lambda: pages.attend(q.transpose(0, 1).contiguous().transpose(0, 1), k, v, 0.1, s)),
+        ("device tensors", lambda: pages.attend(Q, k, v, 0.1, s)),
+        ("device tensors", lambda: pages.free(s.cpu())),
+        ("K: ", lambda: pages.attend(q, k[1:].contiguous(), v, 0.1, s)),
+        ("Q: shape", lambda: pages.attend(q[0], k, v, 0.1, s)),
+    ]:
+        with pytest.raises(ValueError, match=what):
+            call()
+    assert pages.check() == zha.ZHA_OK
+
+
+def test_a_wait_that_runs_out():
+    # the waits for the loads are bounded; here to one clock, which no load keeps
+    zha = _zha()
+    lens = [700 + 100 * i for i in range(40)]
+    pages, Q, K, V, table = _case(zha, 2, 8, 128, 64, 640, lens, 1, BF16, BF16)
+    q, k, v, seqs = Q.cuda(), K.cuda(), V.cuda(), _i32(list(range(40)))
+    want = pages.attend(q, k, v, 0.1, seqs, 0, 640)
+    assert pages.check() == zha.ZHA_OK
+    for _ in range(3):
+        zha.zha_pages_set_wait_limit(pages.handle, 1)
+        lost = pages.attend(q, k, v, 0.1, seqs, 0, 640)
+        assert torch.isnan(lost.float()).all()
+        assert pages.check() == zha.ZHA_ERR_TIMEOUT
+        zha.zha_pages_set_wait_limit(pages.handle, 0)
+        assert torch.equal(pages.attend(q, k, v, 0.1, seqs, 0, 640), want)
+        assert pages.check() == zha.ZHA_OK
+
+
 def test_nothing_to_do():
     zha = _zha()
     pages, Q, K, V, table = _case(zha, 1, 1, 64, 8, 0, [5], 1, F32, F32)

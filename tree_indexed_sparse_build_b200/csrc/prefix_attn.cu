@@ -10,54 +10,77 @@ using namespace zha;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kKeys = 64;  // keys per tile of the fp32 kernel
+constexpr int kKeys = 32;  // keys per tile of the fp32 kernel
 
 // ---------------------------------------------------------------- fp32 kernel
 //
-// A tile of RT rows against 64 keys at a time, everything in fp32 on the FMA pipes: thread
-// (ty, tx) forms the scores of rows ty * RT/16 .. and keys tx, tx + 16, .., keeps those rows'
+// A tile of RT rows against 32 keys at a time, everything in fp32 on the FMA pipes: thread
+// (ty, tx) forms the scores of rows ty * RT/16 .. and keys tx, tx + 16, keeps those rows'
 // running maximum and sum (the 16 threads of a row agree on them by shuffles) and
-// accumulates columns 4 tx .. of the same rows.  K and V take turns in one buffer, so that two
-// CTAs share an SM and one's loads cover the other's arithmetic.
+// accumulates columns 4 tx .. of the same rows.  The next tile's keys and values are on their way in registers,
+// and the page ids of the one after, while a tile is computed; two CTAs share an SM.  (64 keys a tile and one
+// buffer for K and V in turn, loads exposed: 16 sequences of 1,400 tokens 27 us.)
 template <int D, typename TQ, typename TKV>
 struct Fp32Tile {
   static constexpr int kStride = D + 4;  // 16 rows apart by 4 banks: float4 reads without conflicts
   static constexpr int kPStride = kKeys + 4;
+  static constexpr int kVec = 16 / sizeof(TKV), kPer = D / kVec;      // values and vectors of a load, of a row
+  static constexpr int kLoads = (kKeys * kPer + kThreads - 1) / kThreads;  // of a thread, for K and for V
 
-  // Keys [t0, t0 + n) of the sequence whose page ids are `row` to smem; rows past n are zeros.
-  __device__ static void load_keys(const PagesView& v, const TKV* pool, const int* row, int head, int t0, int n,
-                                   float* sm) {
-    constexpr int vec = 16 / sizeof(TKV), per = D / vec;
-    for (int i = threadIdx.x; i < kKeys * per; i += kThreads) {
-      const int r = i / per, c = i % per;
-      float f[vec];
-      if (r < n) {
-        const int t = t0 + r, page = row[t >> v.shift];
-        if ((unsigned)page < (unsigned)v.num_pages) {
-          const TKV* src = pool + (((size_t)page * v.heads + head) * v.page + (t & (v.page - 1))) * D + c * vec;
-          Vec16<TKV>::to_f32(*reinterpret_cast<const uint4*>(src), f);
-        } else {
-          atomicOr(v.err, kDevErrBadSeq);
+  // The next tiles of one segment.
+  struct Ahead {
+    uint4 k[kLoads], v[kLoads];
+    int page[kLoads];  // -1: a row behind the sequence (or a page that is none)
+
+    __device__ __forceinline__ static int row(int i) { return (threadIdx.x + i * kThreads) / kPer; }
+
+    __device__ __forceinline__ void find(const PagesView& v, const int* pages, int t0, int end) {
 #pragma unroll
-          for (int k = 0; k < vec; ++k) f[k] = 0.f;
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < vec; ++k) f[k] = 0.f;
+      for (int i = 0; i < kLoads; ++i) {
+        const int t = t0 + row(i);
+        page[i] = row(i) < kKeys && t < end ? pages[t >> v.shift] : -1;
       }
-#pragma unroll
-      for (int k = 0; k < vec; k += 4)
-        *reinterpret_cast<float4*>(&sm[r * kStride + c * vec + k]) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
     }
-  }
+    __device__ __forceinline__ void load(const PagesView& w, const TKV* K, const TKV* V, int head, int t0) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        k[i] = v[i] = make_uint4(0, 0, 0, 0);
+        if (page[i] == -1) continue;
+        if ((unsigned)page[i] >= (unsigned)w.num_pages) {
+          atomicOr(w.err, kDevErrBadSeq);
+          continue;
+        }
+        const int t = t0 + row(i), c = (threadIdx.x + i * kThreads) % kPer;
+        const size_t at = (((size_t)page[i] * w.heads + head) * w.page + (t & (w.page - 1))) * D + c * kVec;
+        k[i] = *reinterpret_cast<const uint4*>(K + at);
+        v[i] = *reinterpret_cast<const uint4*>(V + at);
+      }
+    }
+    __device__ __forceinline__ static void put(const uint4& x, float* sm) {
+      float f[kVec];
+      Vec16<TKV>::to_f32(x, f);
+#pragma unroll
+      for (int q = 0; q < kVec; q += 4) *reinterpret_cast<float4*>(sm + q) = make_float4(f[q], f[q + 1], f[q + 2], f[q + 3]);
+    }
+    __device__ __forceinline__ void store(float* ks, float* vs) const {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        if (row(i) >= kKeys) continue;
+        const int at = row(i) * kStride + (threadIdx.x + i * kThreads) % kPer * kVec;
+        put(k[i], ks + at);
+        put(v[i], vs + at);
+      }
+    }
+  };
 
   template <int RT>
   __device__ static void segment(const PrefixArgs& a, const Segment& g, float* smem) {
     constexpr int R = RT / 16, C = D / 64;
     const PrefixShape& s = a.s;
     float* qs = smem;
-    float* kv = qs + 64 * kStride;
-    float* ps = kv + kKeys * kStride;
+    float* ks = qs + 64 * kStride;
+    float* vs = ks + kKeys * kStride;
+    float* ps = vs + kKeys * kStride;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
 
     // row r of the tile -> (sequence, row within it)
@@ -76,6 +99,15 @@ struct Fp32Tile {
       *rem = (g.tile % s.tiles_per_seq) * s.prefix_tile + r;
       return *rem < s.rows;
     };
+
+    const int first = g.kind == kOwn ? s.prefix : 0, end = g.len;
+    const int* pages = a.v.table + (size_t)g.pages * a.v.width;
+    const TKV* K = static_cast<const TKV*>(a.K);
+    const TKV* V = static_cast<const TKV*>(a.V);
+    Ahead next;
+    next.find(a.v, pages, first + g.t0 * kKeys, end);
+    next.load(a.v, K, V, g.head, first + g.t0 * kKeys);
+    next.find(a.v, pages, first + (g.t0 + 1) * kKeys, end);
 
     __syncthreads();  // the last segment is done with shared memory
     constexpr int qvec = 16 / sizeof(TQ), qper = D / qvec;
@@ -108,32 +140,32 @@ struct Fp32Tile {
 #pragma unroll
       for (int c = 0; c < 4 * C; ++c) acc[i][c] = 0.f;
     }
-    const int first = g.kind == kOwn ? s.prefix : 0, end = g.len;
-    const int* pages = a.v.table + (size_t)g.pages * a.v.width;
-    const TKV* K = static_cast<const TKV*>(a.K);
-    const TKV* V = static_cast<const TKV*>(a.V);
-
     for (int t = g.t0; t < g.t1; ++t) {
       const int k0 = first + t * kKeys, n = min(kKeys, end - k0);
       __syncthreads();
-      load_keys(a.v, K, pages, g.head, k0, n, kv);
+      next.store(ks, vs);
       __syncthreads();
-      float sc[R][4];
+      if (t + 1 < g.t1) {
+        next.load(a.v, K, V, g.head, k0 + kKeys);
+        next.find(a.v, pages, k0 + 2 * kKeys, end);
+      }
+      constexpr int J = kKeys / 16;
+      float sc[R][J];
 #pragma unroll
       for (int i = 0; i < R; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sc[i][j] = 0.f;
+        for (int j = 0; j < J; ++j) sc[i][j] = 0.f;
 #pragma unroll 4
       for (int c = 0; c < D; c += 4) {
-        float4 q[R], k[4];
+        float4 q[R], k[J];
 #pragma unroll
         for (int i = 0; i < R; ++i) q[i] = *reinterpret_cast<const float4*>(&qs[(ty * R + i) * kStride + c]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const float4*>(&kv[(tx + 16 * j) * kStride + c]);
+        for (int j = 0; j < J; ++j) k[j] = *reinterpret_cast<const float4*>(&ks[(tx + 16 * j) * kStride + c]);
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < J; ++j) {
             sc[i][j] = fmaf(q[i].x, k[j].x, sc[i][j]);
             sc[i][j] = fmaf(q[i].y, k[j].y, sc[i][j]);
             sc[i][j] = fmaf(q[i].z, k[j].z, sc[i][j]);
@@ -144,7 +176,7 @@ struct Fp32Tile {
       for (int i = 0; i < R; ++i) {
         float top = m[i];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < J; ++j) {
           const int key = tx + 16 * j;
           sc[i][j] = key < n && k0 + key < seen[i] ? sc[i][j] * a.scale_log2 : -INFINITY;
           top = fmaxf(top, sc[i][j]);
@@ -155,7 +187,7 @@ struct Fp32Tile {
         const float fix = exp2f(m[i] - base);
         float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < J; ++j) {
           const float p = exp2f(sc[i][j] - base);
           ps[(ty * R + i) * kPStride + tx + 16 * j] = p;
           sum += p;
@@ -167,9 +199,7 @@ struct Fp32Tile {
 #pragma unroll
         for (int c = 0; c < 4 * C; ++c) acc[i][c] *= fix;
       }
-      __syncthreads();
-      load_keys(a.v, V, pages, g.head, k0, n, kv);
-      __syncthreads();
+      __syncwarp();  // a row's weights are written and read by the same half of a warp
 #pragma unroll 4
       for (int key = 0; key < kKeys; ++key) {
         float p[R];
@@ -177,7 +207,7 @@ struct Fp32Tile {
         for (int i = 0; i < R; ++i) p[i] = ps[(ty * R + i) * kPStride + key];
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-          const float4 x = *reinterpret_cast<const float4*>(&kv[key * kStride + 64 * c + 4 * tx]);
+          const float4 x = *reinterpret_cast<const float4*>(&vs[key * kStride + 64 * c + 4 * tx]);
 #pragma unroll
           for (int i = 0; i < R; ++i) {
             acc[i][4 * c + 0] = fmaf(p[i], x.x, acc[i][4 * c + 0]);
@@ -200,7 +230,7 @@ struct Fp32Tile {
     }
   }
 
-  static constexpr size_t kSmem = ((64 + kKeys) * kStride + 64 * kPStride) * sizeof(float);
+  static constexpr size_t kSmem = ((64 + 2 * kKeys) * kStride + 64 * kPStride) * sizeof(float);
 };
 
 template <int D, typename TQ, typename TKV>
@@ -328,7 +358,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
       item(x * s.prefix_keys * kDualCost, s.prefix_keys, kDualCost, 1, 1, (long long)x * s.dual_slot_rows + (rt & 1) * s.prefix_tile + r, s.dual_slot_rows, 0);
     } else {
       const int x = head * s.singles + rt - 2 * s.duals;
-      item(s.dual_total + x * s.prefix_keys * kTileCost, s.prefix_keys, kTileCost, s.streams, s.prefix_parts, s.single_slot0 + (long long)x * s.single_slot_rows + r, s.single_slot_rows,
+      item(s.dual_total + x * s.prefix_keys * s.single_cost, s.prefix_keys, s.single_cost, s.streams, s.prefix_parts, s.single_slot0 + (long long)x * s.single_slot_rows + r, s.single_slot_rows,
            s.single_slot_rows / (s.streams * s.prefix_parts));
     }
   }
@@ -433,11 +463,13 @@ bool plan(const zha_pages* p, int batch, int q_heads, int nq, long long prefix, 
   s->ctas = tensor ? p->sms : 2 * p->sms;
   // all costs, sequences as long as they may be, are counted in 31 bits
   const long long most = (long long)p->desc.max_seq_pages * p->desc.page_tokens;
-  if ((long long)heads * row_tiles * s->prefix_keys * kDualCost +
+  // fp32: the arithmetic of 64 rows takes about three times that of 16
+  s->single_cost = !tensor && s->prefix_tile > s->own_tile ? 3 * kTileCost : kTileCost;
+  if ((long long)heads * row_tiles * s->prefix_keys * (kDualCost + s->single_cost) +
           (long long)batch * heads * s->own_tiles * (ceil_div(most, s->tile_keys) * kTileCost + kOwnStart) > 0x7fffffffLL)
     return false;
   s->dual_total = heads * s->duals * s->prefix_keys * kDualCost;
-  s->prefix_total = s->dual_total + heads * s->singles * s->prefix_keys * kTileCost;
+  s->prefix_total = s->dual_total + heads * s->singles * s->prefix_keys * s->single_cost;
   s->dual_slot_rows = 2 * s->prefix_tile;
   const int single_rows = s->prefix_parts == 4 ? (int)rows * batch : s->prefix_tile;
   s->single_slot_rows = s->streams * s->prefix_parts * single_rows;

@@ -37,6 +37,7 @@ struct PrefixShape {
   int streams;         // streams of a single or own item's segment (1, or 2 in the tensor kernel)
   int prefix_keys;     // key tiles of the prefix
   int ctas;
+  int single_cost;               // of a key tile of a single item
   int dual_total, prefix_total;  // cost of all dual items, of all prefix items
   int dual_slot_rows, single_slot_rows, own_slot_rows;
   long long single_slot0, own_slot0;   // first row of the single and of the own slots
@@ -62,7 +63,7 @@ __device__ __forceinline__ int prefix_len(const PrefixArgs& a, int b, int* slot)
   const int x = a.seqs[b];
   *slot = x;
   if ((unsigned)x >= (unsigned)a.v.max_seqs) return 0;
-  return a.v.lens[x];
+  return max(0, min(a.v.lens[x], a.v.width << a.v.shift));
 }
 
 __device__ __forceinline__ int own_key_tiles(const PrefixShape& s, int len) {
@@ -119,7 +120,7 @@ struct Walk {
     const PrefixShape& s = a.s;
     while (pos < hi && pos < s.prefix_total) {
       const bool dual = pos < s.dual_total;
-      const int w = dual ? kDualCost : kTileCost, per_head = dual ? s.duals : s.singles, origin = dual ? 0 : s.dual_total;
+      const int w = dual ? kDualCost : s.single_cost, per_head = dual ? s.duals : s.singles, origin = dual ? 0 : s.dual_total;
       const int len_w = s.prefix_keys * w, i = (pos - origin) / len_w, start = origin + i * len_w;
       g->t0 = tiles_before(pos, start, s.prefix_keys, w);
       g->t1 = tiles_before(hi, start, s.prefix_keys, w);
@@ -181,77 +182,86 @@ __device__ __forceinline__ Walk find_share(const PrefixArgs& a, int cta, int thr
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = threads / 32;
   const int group = s.heads * s.own_tiles;
   int* out = sm + warps;  // sequence, cost before it, its tokens and slot
+  // sums of the own costs before this thread's entry of a round of `threads` (lane, then warp)
+  int before = 0, total = 0;
+  auto round = [&](int cost) {
+    int v = cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    if (lane == 31) sm[warp] = v;
+    __syncthreads();
+    before = total + v - cost;
+    for (int i = 0; i < warps; ++i) {
+      before += i < warp ? sm[i] : 0;
+      total += sm[i];
+    }
+  };
+  auto entry = [&](int b, int* slot) {
+    int len = 0;
+    *slot = 0;
+    if (b < s.batch) {
+      len = prefix_len(a, b, slot);
+      if (cta == 0) {
+        a.cum[s.batch + 1 + b] = len;
+        if ((unsigned)*slot >= (unsigned)a.v.max_seqs) atomicOr(a.v.err, kDevErrBadSeq);
+      }
+    }
+    return len;
+  };
   // the total first: a share's borders depend on it
-  int total = 0, mine = 0, len_first = 0, slot_first = 0;
-  for (int b = tid; b < s.batch; b += threads) {
-    int slot;
-    const int len = prefix_len(a, b, &slot);
-    mine += own_cost(s, len);
-    if (b == tid) {
-      len_first = len;
-      slot_first = slot;
-    }
-    if (cta == 0) {
-      a.cum[s.batch + 1 + b] = len;
-      if ((unsigned)slot >= (unsigned)a.v.max_seqs) atomicOr(a.v.err, kDevErrBadSeq);
-    }
+  int slot, len = entry(tid, &slot);
+  round(own_cost(s, len));
+  for (int b0 = threads; b0 < s.batch; b0 += threads) {
+    int x;
+    const int l = entry(b0 + tid, &x);
+    __syncthreads();
+    round(own_cost(s, l));
   }
-  mine = __reduce_add_sync(0xffffffffu, mine);
-  if (lane == 0) sm[warp] = mine;
-  __syncthreads();
-  for (int i = 0; i < warps; ++i) total += sm[i];
-  __syncthreads();
-  const int T = s.prefix_total + total * group;
+  const int all = total, T = s.prefix_total + all * group;
   Walk w;
   w.pos = share_start(cta, T, s.ctas);
   w.hi = share_start(cta + 1, T, s.ctas);
   w.b = w.n = w.item = w.at = w.len = w.pages = w.next_len = w.next_pages = 0;
   if (cta == 0 && tid == 0) {
-    a.cum[s.batch] = total;
+    a.cum[s.batch] = all;
     if (s.prefix > 0 && a.v.lens[s.prefix_seq] < s.prefix) atomicOr(a.v.err, kDevErrBadSeq);
   }
   // the sequence at the share's start (or the first one, if the share starts in the prefix)
-  const int x = max(0, w.pos - s.prefix_total);
-  if (w.hi > s.prefix_total || cta == 0) {
-    int carry = 0;
+  const bool find = w.pos < w.hi && w.hi > s.prefix_total;
+  if (find || cta == 0) {
+    const int x = max(0, w.pos - s.prefix_total);
+    const bool again = s.batch > threads;  // (else the sums of the only round still stand)
+    if (again) total = 0;
     for (int b0 = 0; b0 < s.batch; b0 += threads) {
-      const int b = b0 + tid;
-      int slot = slot_first, len = len_first;
-      if (b0 > 0) len = b < s.batch ? prefix_len(a, b, &slot) : 0;
-      const int n = own_cost(s, len);
-      int v = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += y;
+      if (again) {
+        len = entry(b0 + tid, &slot);
+        __syncthreads();
+        round(own_cost(s, len));
       }
-      if (lane == 31) sm[warp] = v;
-      __syncthreads();
-      int before = carry + v - n;
-      for (int i = 0; i < warps; ++i) {
-        before += i < warp ? sm[i] : 0;
-        carry += sm[i];
-      }
+      const int b = b0 + tid, cost = own_cost(s, len);
       if (b < s.batch) {
         if (cta == 0) a.cum[b] = before;
-        if (x >= before * group && x < (before + n) * group) {
+        if (x >= before * group && x < (before + cost) * group) {
           out[0] = b;
           out[1] = before;
           out[2] = len;
           out[3] = slot;
         }
       }
-      __syncthreads();
-      if (cta != 0 && carry * group > x) break;
+      if (cta != 0 && total * group > x) break;
     }
-    if (w.pos < w.hi && w.hi > s.prefix_total) {  // (nothing is written to `out` for an empty share)
+    __syncthreads();
+    if (find) {  // (nothing is written to `out` for an empty share)
       w.b = out[0];
       w.len = out[2];
       w.pages = out[3];
       w.n = own_key_tiles(s, w.len);
-      const int before = out[1] * group, cost = w.n * kTileCost + kOwnStart;
-      w.item = (x - before) / cost;
-      w.at = s.prefix_total + before + w.item * cost + kOwnStart;
+      const int start = out[1] * group, cost = w.n * kTileCost + kOwnStart;
+      w.item = (x - start) / cost;
+      w.at = s.prefix_total + start + w.item * cost + kOwnStart;
       w.fetch(a);
     }
     __syncthreads();
