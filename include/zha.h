@@ -401,7 +401,7 @@ zha_status zha_pages_gather(const zha_pages* pages, const void* d_K, const void*
  * counts as an empty sequence, a page id out of range as a page of zeros; those, and a prefix longer than
  * prefix_seq, set ZHA_ERR_DEVICE.  Values of tokens that any query of a call sees must be finite.
  * bf16 queries over a bf16 cache run on the tensor cores: products are exact, sums fp32; for a bf16 output
- * the softmax weights are rounded to bf16 before they meet V, for an fp32 output they keep 16 bits.
+ * the softmax weights are rounded to bf16 before they meet V, for an fp32 output they keep 24 bits.
  * All other types run in fp32. */
 size_t zha_prefix_attn_scratch_bytes(const zha_pages* pages, int batch, int q_heads, int nq, long long prefix_tokens);
 zha_status zha_prefix_attn_decode(const zha_pages* pages, const void* d_Q, zha_dtype q_dtype, int batch, int q_heads,

@@ -428,7 +428,8 @@ cudaError_t launch_join(const PrefixArgs& a, zha_dtype o, cudaStream_t s) {
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // The cut of a call.  Returns false on sizes outside the kernels' index ranges.
-bool plan(const zha_pages* p, int batch, int q_heads, int nq, long long prefix, bool tensor, PrefixShape* s) {
+// wide: tensor kernel with an fp32 output.
+bool plan(const zha_pages* p, int batch, int q_heads, int nq, long long prefix, bool tensor, bool wide, PrefixShape* s) {
   const int heads = p->desc.kv_heads;
   if (batch < 1 || nq < 1 || q_heads < 1 || q_heads % heads) return false;
   const long long rows = (long long)(q_heads / heads) * nq;
@@ -439,7 +440,7 @@ bool plan(const zha_pages* p, int batch, int q_heads, int nq, long long prefix, 
   s->rows = (int)rows;
   s->nq = nq;
   s->prefix = (int)prefix;
-  s->tile_keys = tensor ? 128 : kKeys;
+  s->tile_keys = !tensor ? kKeys : wide ? 64 : 128;
   // fp32: 16 rows at a time where there are no more, else 64 (the arithmetic is per tile row)
   s->prefix_tile = tensor ? 128 : rows * batch <= 16 ? 16 : 64;
   s->own_tile = tensor ? 128 : rows <= 16 ? 16 : 64;
@@ -507,9 +508,9 @@ size_t zha_prefix_attn_scratch_bytes(const zha_pages* p, int batch, int q_heads,
   if (!p || prefix_tokens < 0 || prefix_tokens > 1LL << 30) return 0;
   PrefixShape s;
   size_t most = 0;
-  for (int tensor = 0; tensor < 2; ++tensor) {  // whatever the queries' type
-    if (tensor && p->desc.kv_dtype != ZHA_BF16) break;
-    if (!plan(p, batch, q_heads, nq, prefix_tokens, tensor != 0, &s)) return 0;
+  for (int kind = 0; kind < 3; ++kind) {  // whatever the queries' and the output's type
+    if (kind && p->desc.kv_dtype != ZHA_BF16) break;
+    if (!plan(p, batch, q_heads, nq, prefix_tokens, kind > 0, kind > 1, &s)) return 0;
     const size_t n = scratch_of(p, s).bytes;
     if (n > most) most = n;
   }
@@ -535,7 +536,7 @@ zha_status zha_prefix_attn_decode(const zha_pages* p, const void* d_Q, zha_dtype
     return ZHA_ERR_INVALID_ARG;
   PrefixArgs a;
   const bool tensor = tensor_path(p, q_dtype);
-  if (!plan(p, batch, q_heads, nq, prefix_tokens, tensor, &a.s)) return ZHA_ERR_UNSUPPORTED;
+  if (!plan(p, batch, q_heads, nq, prefix_tokens, tensor, o_dtype == ZHA_F32, &a.s)) return ZHA_ERR_UNSUPPORTED;
   if (scratch_bytes < zha_prefix_attn_scratch_bytes(p, batch, q_heads, nq, prefix_tokens)) return ZHA_ERR_INVALID_ARG;
   const Scratch x = scratch_of(p, a.s);
   char* base = static_cast<char*>(d_scratch);

@@ -35,7 +35,10 @@ using namespace zha;
 
 namespace {
 
-constexpr int kRows = 128, kKeys = 128;
+constexpr int kRows = 128;
+// Keys of a tile.  An fp32 output wants the weights in 24 bits: three bf16 numbers each, whose three MMAs with V
+// find room in S only for 64 keys.  (Two numbers for 128 keys were off by 1.5e-6 of the output.)
+__host__ __device__ constexpr int keys_of(bool wide) { return wide ? 64 : 128; }
 constexpr int kThreads = 384;
 constexpr int kTmemCols = 512;
 constexpr int kByFma = 2;     // of 16 pairs of weights, those whose exp2 the FMA pipes compute
@@ -116,8 +119,8 @@ struct Tiles {
     t = g.t0;
   }
   __device__ __forceinline__ bool dual() const { return g.kind == kDual; }
-  __device__ __forceinline__ int k0(const PrefixArgs& a) const { return (g.kind == kOwn ? a.s.prefix : 0) + t * kKeys; }
-  __device__ __forceinline__ int keys(const PrefixArgs& a) const { return min(kKeys, g.len - k0(a)); }
+  __device__ __forceinline__ int k0(const PrefixArgs& a) const { return (g.kind == kOwn ? a.s.prefix : 0) + t * a.s.tile_keys; }
+  __device__ __forceinline__ int keys(const PrefixArgs& a) const { return min(a.s.tile_keys, g.len - k0(a)); }
   __device__ __forceinline__ void step(const PrefixArgs& a, int cta) {
     if (++t == g.t1) {
       any = w.next(a, cta, &g);
@@ -164,7 +167,7 @@ struct Loader {
 
   __device__ __forceinline__ Loader(const TcArgs& x, Bars& b, const Waiter& w, uint32_t q, uint32_t kv)
       : args(x), a(x.a), bars(b), wait(w), q_smem(q), ring(kv), lane(threadIdx.x & 31) {
-    per_tile = kKeys >> args.chunk_shift;
+    per_tile = a.s.tile_keys >> args.chunk_shift;
     chunk = lane % per_tile;
     half = lane / per_tile;
     mine = lane < per_tile * (D / 64);
@@ -336,10 +339,13 @@ struct Issuer {
         if (started) {
           constexpr uint32_t od = mma_desc(128, D, true);
 #pragma unroll
-          for (int x = 0; x < kKeys / 16; ++x) {
+          for (int x = 0; x < keys_of(WIDE) / 16; ++x) {
             if (x >= steps) break;
             mma_ts(o_tmem, s_tmem + x * 8, desc_of(vd + x * 128, C::kHalf), od, add || x > 0);
-            if (WIDE) mma_ts(o_tmem, s_tmem + 64 + x * 8, desc_of(vd + x * 128, C::kHalf), od, true);
+            if (WIDE) {
+              mma_ts(o_tmem, s_tmem + 32 + x * 8, desc_of(vd + x * 128, C::kHalf), od, true);
+              mma_ts(o_tmem, s_tmem + 64 + x * 8, desc_of(vd + x * 128, C::kHalf), od, true);
+            }
           }
           mma_commit(&bars.v_empty[vp.stage]);
           if (!(v.y & kPaired)) mma_commit(&bars.v_empty[vp.stage]);
@@ -401,14 +407,27 @@ struct Stream {
 
   float m, l;  // of this thread's row: what its weights refer to, their sum
 
+  // N columns of P.
+  template <int N>
+  __device__ __forceinline__ void put(int col, const uint32_t* w) {
+    if constexpr (N == 16)
+      tmem_st16(ts + col, w);
+    else
+      tmem_st8(ts + col, w);
+  }
+
   // Weights of COLS keys: scores at S columns [col, col + COLS), of which the first lim count.  O is
   // rescaled when the maximum moves (`fresh`: there is none yet).
   template <int COLS>
   __device__ __forceinline__ void weigh(int col, int lim, bool fresh) {
     const float c = a.scale_log2;
     uint32_t x[COLS];
+    if constexpr (COLS == 16) {
+      tmem_ld16(x, ts + col);
+    } else {
 #pragma unroll
-    for (int q = 0; q < COLS / 32; ++q) tmem_ld32(x + 32 * q, ts + col + 32 * q);
+      for (int q = 0; q < COLS / 32; ++q) tmem_ld32(x + 32 * q, ts + col + 32 * q);
+    }
     tmem_wait_ld();
     if (args.flip) {
 #pragma unroll
@@ -447,14 +466,16 @@ struct Stream {
     const float off = m == -INFINITY ? 0.f : -m;
     const uint64_t cc = pair(c, c), oo = pair(off, off);
     uint64_t sum = pair(0.f, 0.f);
+    constexpr int G = COLS < 32 ? COLS / 2 : 16;  // packed columns at a time
 #pragma unroll
-    for (int q = 0; q < COLS / 32; ++q) {
-      uint32_t hi[16], lo[16];
+    for (int q = 0; q < COLS / 2 / G; ++q) {
+      uint32_t hi[G], mid[G], lo[G];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
+      for (int k = 0; k < G; ++k) {
         float p0, p1;
-        const uint64_t e = fma2(pair(__uint_as_float(x[32 * q + 2 * k]), __uint_as_float(x[32 * q + 2 * k + 1])), cc, oo);
-        if (!WIDE && k % 16 < kByFma) {
+        const int at = 2 * (q * G + k);
+        const uint64_t e = fma2(pair(__uint_as_float(x[at]), __uint_as_float(x[at + 1])), cc, oo);
+        if (!WIDE && k < kByFma) {
           exp2_by_fma(e, &p0, &p1);
         } else {
           split(e, &p0, &p1);
@@ -463,10 +484,18 @@ struct Stream {
         }
         sum = add2(sum, pair(p0, p1));
         hi[k] = pack_bf16(p0, p1);
-        if (WIDE) lo[k] = pack_bf16(p0 - __uint_as_float(hi[k] << 16), p1 - __uint_as_float(hi[k] & 0xffff0000u));
+        if (WIDE) {  // what a rounding leaves is exact in fp32
+          p0 -= __uint_as_float(hi[k] << 16);
+          p1 -= __uint_as_float(hi[k] & 0xffff0000u);
+          mid[k] = pack_bf16(p0, p1);
+          lo[k] = pack_bf16(p0 - __uint_as_float(mid[k] << 16), p1 - __uint_as_float(mid[k] & 0xffff0000u));
+        }
       }
-      tmem_st16(ts + col / 2 + 16 * q, hi);
-      if (WIDE) tmem_st16(ts + 64 + col / 2 + 16 * q, lo);
+      put<G>(col / 2 + G * q, hi);
+      if (WIDE) {
+        put<G>(32 + col / 2 + G * q, mid);
+        put<G>(64 + col / 2 + G * q, lo);
+      }
     }
     float s0, s1;
     split(sum, &s0, &s1);
@@ -475,17 +504,22 @@ struct Stream {
 
   // Zeros for the other warps' quarters of the keys.
   __device__ __forceinline__ void clear_others() {
+    constexpr int G = keys_of(WIDE) / 8;
     const uint32_t z[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       if (q != quarter) {
-        tmem_st16(ts + 16 * q, z);
-        if (WIDE) tmem_st16(ts + 64 + 16 * q, z);
+        put<G>(G * q, z);
+        if (WIDE) {
+          put<G>(32 + G * q, z);
+          put<G>(64 + G * q, z);
+        }
       }
   }
 
   // This stream's tiles j0, j0 + by, .. of a segment that starts with the share's tile `tile0`.
   __device__ __forceinline__ bool segment(const Segment& g, int j0, int by, uint32_t tile0) {
+    constexpr int kKeys = keys_of(WIDE), kQuarter = kKeys / 4;
     const PrefixShape& s = a.s;
     const int n = g.t1 - g.t0;
     const int parts = g.kind == kOwn ? s.own_parts : g.kind == kSingle ? s.prefix_parts : 1;
@@ -522,7 +556,7 @@ struct Stream {
     m = -INFINITY;
     l = 0.f;
     for (int j = j0; j < n; j += by) {
-      const int k0 = first + (g.t0 + j) * kKeys, left = min(kKeys, g.len - k0);
+      const int k0 = first + (g.t0 + j) * kKeys, left = min(kKeys, g.len - k0);  // first key, keys
       if (!wait(&bars.s_full[st], ns++ & 1)) return false;
       tc_fence_after();
       if (left & 15) {  // rows of V behind the sequence, up to the end of the last MMA's 16
@@ -540,11 +574,11 @@ struct Stream {
       }
       if (work) {
         if (parts == 4) {
-          weigh<32>(32 * quarter, row_end - k0 - 32 * quarter, j == j0);
+          weigh<kQuarter>(kQuarter * quarter, row_end - k0 - kQuarter * quarter, j == j0);
           __syncwarp();
           clear_others();
         } else {
-          weigh<128>(0, row_end - k0, j == j0);
+          weigh<kKeys>(0, row_end - k0, j == j0);
         }
         tmem_wait_st();
       }
@@ -728,7 +762,7 @@ cudaError_t launch_prefix_tc(const zha_pages* p, const PrefixArgs& a, int head_d
   const cuuint32_t own[4] = {64, rows, 1, 1};
   const int together = s.prefix_parts == 4 ? s.batch : s.seqs_per_tile ? s.seqs_per_tile : 1;
   const cuuint32_t shared[4] = {64, rows, 1, (cuuint32_t)together};
-  x.chunk = p->desc.page_tokens < kKeys ? p->desc.page_tokens : kKeys;
+  x.chunk = p->desc.page_tokens < s.tile_keys ? p->desc.page_tokens : s.tile_keys;
   x.chunk_shift = 0;
   while ((1 << x.chunk_shift) < x.chunk) ++x.chunk_shift;
   const cuuint64_t kv[3] = {d, (cuuint64_t)p->desc.page_tokens, (cuuint64_t)p->desc.num_pages * s.heads};
