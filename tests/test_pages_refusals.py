@@ -21,8 +21,8 @@ def _desc(**kw):
 
 def test_workspace_size():
     # a 64-word header, eight arrays of max_seqs, five of num_pages, the bitmap and the table
-    assert zha.zha_pages_workspace_bytes(_desc()) == 256 * (1 + 8 + 4 + 1 + 1)
-    assert zha.zha_pages_workspace_bytes(_desc(max_seqs=100, max_seq_pages=1000)) == 256 + 8 * 512 + 5 * 256 + 400128
+    assert zha.zha_pages_workspace_bytes(_desc()) == 256 * (1 + 8 + 5 + 1 + 1)
+    assert zha.zha_pages_workspace_bytes(_desc(max_seqs=100, max_seq_pages=1000)) == 256 + 8 * 512 + 5 * 256 + 256 + 400128
 
 
 @pytest.mark.parametrize("bad,status", [

@@ -519,17 +519,20 @@ def zha_pages_refs(handle) -> int:
 def _pools(d: zha_pages_desc, *pools, names="KV") -> None:
     """Refuse a pool of another type or size than [num_pages, kv_heads, page_tokens, head_dim]."""
     n = d.num_pages * d.kv_heads * d.page_tokens * d.head_dim
+    dtype = _TORCH_DT[d.kv_dtype]
     for name, t in zip(names, pools):
-        if t.dtype != _TORCH_DT[d.kv_dtype]:
-            raise ValueError(f"{name}: dtype {t.dtype}, the cache's pools are {_TORCH_DT[d.kv_dtype]}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name}: dtype {t.dtype}, the cache's pools are {dtype}")
         if t.numel() != n:
             raise ValueError(f"{name}: {t.numel()} elements, the cache's [num_pages, kv_heads, page_tokens, "
                              f"head_dim] pool has {n}")
 
 
 def _slots(seqs: torch.Tensor, what: str, n: int | None = None) -> int:
-    _expect(seqs, what, seqs.numel() if n is None else n, _I32)
-    return seqs.numel()
+    count = seqs.numel()
+    if seqs.dtype != torch.int32 or (n is not None and count != n):
+        _expect(seqs, what, count if n is None else n, _I32)
+    return count
 
 
 def _rows(d: zha_pages_desc, n: int, K: torch.Tensor, V: torch.Tensor, what: str) -> int:
@@ -945,11 +948,17 @@ class Pages:
                out_dtype: torch.dtype = torch.bfloat16, O: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """Attention of Q [batch, q_heads, nq, head_dim] over slots seqs [batch], whose first
         prefix_tokens tokens are the pages of slot prefix_seq."""
-        need = zha_prefix_attn_scratch_bytes(self.handle, Q.shape[0], Q.shape[1], Q.shape[2], prefix_tokens)
-        with _allocating(stream):
-            if O is None:
-                O = torch.empty(Q.shape, dtype=out_dtype, device=Q.device)
-            scratch = torch.empty(max(need, 16), dtype=torch.uint8, device=Q.device)
+        if Q.dim() != 4:
+            raise ValueError(f"Q: shape {tuple(Q.shape)}, expected [batch, q_heads, nq, {self.desc.head_dim}]")
+        B, Hq, nq, _ = Q.shape
+        need = lib().zha_prefix_attn_scratch_bytes(self.handle, B, Hq, nq, prefix_tokens)
+        if stream is None:  # (the usual call, without the context's 2 us)
+            O = Q.new_empty(Q.shape, dtype=out_dtype) if O is None else O
+            scratch = Q.new_empty((need + 16,), dtype=torch.uint8)
+        else:
+            with _allocating(stream):
+                O = Q.new_empty(Q.shape, dtype=out_dtype) if O is None else O
+                scratch = Q.new_empty((need + 16,), dtype=torch.uint8)
         zha_prefix_attn_decode(self.handle, Q, K, V, seqs, prefix_seq, prefix_tokens, causal, scale, O, scratch, stream)
         return O
 
