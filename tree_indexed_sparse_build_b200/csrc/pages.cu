@@ -713,7 +713,9 @@ __global__ void __launch_bounds__(kRowThreads) load_apply_kernel(PagesView d, co
       if (more) atomicAdd(d.free_pages, more);
     }
   }
-  // the last CTA to leave (all have looked) puts the flag back
+  // the last CTA to leave puts the flag back, when every thread of every CTA has looked
+  __syncthreads();
+  __threadfence();
   if (threadIdx.x == 0 && atomicAdd(d.ticket, 1) == (int)gridDim.x - 1) {
     *d.ticket = 0;
     *d.load_bad = 0;
@@ -925,7 +927,9 @@ zha_status zha_pages_copy(const zha_pages* from, const void* d_Kfrom, const void
   const RowArgs x = {p->v, from->v, d_src, d_dst, nullptr, n, 0, (const uint4*)d_Kfrom, (const uint4*)d_Vfrom, (uint4*)d_K,
                      (uint4*)d_V};
   const long long page = 32LL * p->v.page * p->v.heads * p->v.row_vecs;
-  return launch_rows<kCopy>(p, x, n * p->desc.max_seq_pages * page,
+  // (a copy moves no more pages than the pool has)
+  const long long most = (long long)n * p->desc.max_seq_pages, pool = p->desc.num_pages;
+  return launch_rows<kCopy>(p, x, (most < pool ? most : pool) * page,
                             row_grid(p, n, (long long)p->desc.max_seq_pages * p->desc.kv_heads, kRowWarps), stream);
 }
 
