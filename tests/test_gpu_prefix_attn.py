@@ -5,7 +5,7 @@ core's sums, which may truncate), a score of d products is off by at most (d + 3
 products' sizes (a), and exp2 by a few u, so a weight is off by a factor within 1 +- e, e = (d + 3) u a +
 8 u; numerator and denominator are sums of n weights, each off by n u more.  The output is off by at most
 (2 e + 2 (n + 64) u) sum(p |v|).  Weights rounded to bf16 for the product with V add 2^-8 of that sum,
-weights kept as three bf16 numbers 2^-24, and a bf16 output half a step, 2^-8 of itself.  (A quarter of the weights for
+weights kept as three bf16 numbers 2^-24, and a bf16 output half a step, 2^-8 of itself.  (An eighth of the weights for
 a bf16 output have an exp2 that is off by 1.1e-4 of itself, which is 3% of that rounding and added.)
 """
 from __future__ import annotations
@@ -151,6 +151,53 @@ def test_growing_maximum(types):
     Q = (Q.float().abs()).to(q)
     got = pages.attend(Q.cuda(), K.cuda(), V.cuda(), 1.0, _i32([0, 1]), 0, 512, False, out)
     _compare(got, Q, K, V, table, [512, 1500], [0, 1], 1.0, 0, 512, False, kv, q, out)
+
+
+@pytest.mark.parametrize("own", [1, 200])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("types", TYPES, ids=lambda t: "-".join(str(x)[6:] for x in t))
+def test_a_nan_reaches_the_rows_that_see_it_and_no_others(types, value, own):
+    # a score that is NaN, or infinite, of the only key behind the prefix or of one of many; and a query row that is NaN
+    zha = _zha()
+    kv, q, out = types
+    lens = [256 + own, 300, 256, 290]
+    pages, Q, K, V, table = _case(zha, 2, 2, 64, 16, 256, lens, 1, kv, q)
+    last = lens[0] - 1
+    Qn = Q.clone()
+    if value == value:  # one infinite product, positive
+        Qn[0, :, :, 0] = Qn[0, :, :, 0].abs() + 1
+        K[int(table[0, last // 16]), :, last % 16, 0] = value
+    else:
+        K[int(table[0, last // 16]), :, last % 16] = value
+    Qn[3, 1] = float("nan")
+    seqs = [0, 1, 2, 3]
+    got = pages.attend(Qn.cuda(), K.cuda(), V.cuda(), 0.125, _i32(seqs), 0, 256, False, out)
+    assert pages.check() == zha.ZHA_OK
+    assert torch.isnan(got[0]).all() and torch.isnan(got[3, 1]).all()
+    K[int(table[0, last // 16]), :, last % 16] = 0
+    o, w, a = attend64(Q, K, V, table, lens, seqs, 0.125, 0, 256, False)
+    keep = np.ones(o.shape[:2], dtype=bool)
+    keep[0] = keep[3, 1] = False
+    off = np.abs(got.double().cpu().numpy() - o)
+    lim = _bound(o, w, a, 64, max(lens), kv == BF16 and q == BF16, out)
+    assert (off <= lim)[keep].all()
+
+
+@pytest.mark.parametrize("types", TYPES, ids=lambda t: "-".join(str(x)[6:] for x in t))
+def test_masked_values_of_any_size_weigh_nothing(types):
+    # tokens that only later queries of a sequence see hold the largest finite values
+    zha = _zha()
+    kv, q, out = types
+    lens, nq = [261, 290, 140], 5
+    pages, Q, K, V, table = _case(zha, 2, 2, 64, 16, 128, lens, nq, kv, q)
+    K2, V2 = K.clone(), V.clone()
+    for s, n in enumerate(lens):
+        for t in range(n - nq + 1, n):
+            V2[int(table[s, t // 16]), :, t % 16] = 3e38
+    seqs = [0, 1, 2]
+    got = [pages.attend(Q.cuda(), K.cuda(), v.cuda(), 0.125, _i32(seqs), 0, 128, True, out) for v in (V, V2)]
+    assert pages.check() == zha.ZHA_OK
+    assert torch.equal(got[0][:, :, 0], got[1][:, :, 0])
 
 
 def test_random_shapes():

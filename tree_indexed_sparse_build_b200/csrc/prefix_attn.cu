@@ -270,15 +270,16 @@ struct Joined {
     float top = m;
 #pragma unroll
     for (int k = 0; k < K; ++k) top = fmaxf(top, ml[k].x);
-    if (top == -INFINITY) return;
-    float f = exp2f(m - top);
+    // (not left out if it is -inf: the sum of scores that are all NaN is NaN, and has to come through)
+    const float base = top == -INFINITY ? 0.f : top;
+    float f = exp2f(m - base);
     m = top;
     l *= f;
 #pragma unroll
     for (int c = 0; c < N; ++c) acc[c] *= f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      f = exp2f(ml[k].x - top);
+      f = exp2f(ml[k].x - base);
       l += ml[k].y * f;
 #pragma unroll
       for (int c = 0; c < N; ++c) acc[c] += x[k][c] * f;

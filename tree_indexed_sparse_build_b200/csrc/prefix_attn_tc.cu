@@ -297,8 +297,7 @@ struct Issuer {
   // This stream's tiles: S of the first, then again and again O += P V of one and S of the next.  A tile's keys are
   // released by two arrivals, its queries too: one of each stream, or two of the only one that uses them.
   //
-  // An issuer waits for a ring place whose stage held, three (keys; values: two, the stream's own) tiles
-  // before, a tile of the other stream.  A parity says that a phase is over only to somebody who knows that
+  // A stage of a ring may have held, a round before, a tile of the other stream.  A parity says that a phase is over only to somebody who knows that
   // the phase before is.  Here the turns say so: the other stream issued its scores of that tile before it gave
   // up the turn that this stream used last.
   __device__ __forceinline__ bool run(bool pairs) {
@@ -443,11 +442,13 @@ struct Stream {
       t0 = max3(t0, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
       if (k + 3 < COLS) t1 = max3(t1, __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
     }
-    const float top = fmaxf(t0, t1) * c;
+    // a score that is NaN or +inf makes the row NaN, by way of the maximum
+    float top = max3(t0, t1, t1) * c;
+    if (top == INFINITY) top = NAN;
     float fix = 1.f;
     if (m == -INFINITY) {
       m = top;  // nothing of this row in O yet
-    } else if (top > m + kSlack) {
+    } else if (!(top <= m + kSlack)) {
       fix = exp2_approx(m - top);
       m = top;
     }

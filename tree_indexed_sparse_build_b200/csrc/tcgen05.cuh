@@ -132,9 +132,10 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 constexpr float kExp2C0 = 0.999924541f, kExp2C1 = 0.693136752f, kExp2C2 = 0.242639482f, kExp2C3 = 0.0558382832f;
+// The largest of three, NaN if one of them is.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 // Two fp32 operations in one instruction.
@@ -158,12 +159,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 // 2^x of two floats on the FMA pipes, for x <= 8 or so: x is split into the nearest integer n, read off the low
 // bits of x + 1.5 * 2^23, and the rest f in [-1/2, 1/2]; 2^f is a cubic through Chebyshev nodes of
-// that interval, off by less than 1.1e-4 of itself; n is added to the exponent.  x below -126 gives
-// 2^-126, which no sum of weights sees.
+// that interval, off by less than 1.1e-4 of itself; n is added to the exponent.  x below -125 (a masked score) counts as
+// -125, and what that gives is taken off all results: exactly zero for those, nothing that others see.  A NaN
+// is lost here; the caller's maximum keeps it.
 __device__ __forceinline__ void exp2_by_fma(uint64_t x, float* lo, float* hi) {
   float a, b;
   split(x, &a, &b);
-  x = pair(fmaxf(a, -126.f), fmaxf(b, -126.f));
+  x = pair(fmaxf(a, -125.f), fmaxf(b, -125.f));
   const uint64_t n = add2(x, pair(12582912.f, 12582912.f));
   const uint64_t f = fma2(add2(n, pair(-12582912.f, -12582912.f)), pair(-1.f, -1.f), x);
   uint64_t p = fma2(f, pair(kExp2C3, kExp2C3), pair(kExp2C2, kExp2C2));
@@ -172,8 +174,10 @@ __device__ __forceinline__ void exp2_by_fma(uint64_t x, float* lo, float* hi) {
   float na, nb, pa, pb;
   split(n, &na, &nb);
   split(p, &pa, &pb);
-  *lo = __uint_as_float(__float_as_uint(pa) + (__float_as_uint(na) << 23));
-  *hi = __uint_as_float(__float_as_uint(pb) + (__float_as_uint(nb) << 23));
+  pa = __uint_as_float(__float_as_uint(pa) + (__float_as_uint(na) << 23));
+  pb = __uint_as_float(__float_as_uint(pb) + (__float_as_uint(nb) << 23));
+  constexpr float least = kExp2C0 * 0x1p-125f;
+  split(add2(pair(pa, pb), pair(-least, -least)), lo, hi);
 }
 // Two floats to bf16 (nearest even): lo in the low half.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
