@@ -216,6 +216,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PagesView d, PagesVi
 
 // ---------------------------------------------------------------- rows
 
+// The row kernels move bytes and are bound by them where there are many: each vector is read and written once, eight
+// loads in flight per thread.  At 8 KV heads of 128 in bf16, bytes read and written: 36,000 ragged tokens appended in
+// 54 us (5.5 TB/s; the plan before takes 5 us) and gathered in 51 us (5.8), 125,000 tokens copied in 168 us (6.1) and compacted
+// in 165 us (6.2).
+
 // One warp copies n 16-byte vectors of K and of V; eight loads in flight per lane.
 __device__ __forceinline__ void warp_copy(const uint4* ks, const uint4* vs, uint4* kd, uint4* vd, int n, int lane) {
   constexpr int U = 4;
@@ -811,10 +816,11 @@ unsigned column_grid(const zha_pages* p) {
   return (unsigned)(g < 2 * p->sms ? g : 2 * p->sms);
 }
 
-// CTAs over blockIdx.x so that `entries` list entries fill the device about eight CTAs deep,
-// and no more than `items` units of work per CTA could use.
+// CTAs over blockIdx.x so that `entries` list entries fill the device about 16 CTAs deep, and no more than `items`
+// units of work per CTA could use.  Eight of them are resident: a long entry's others take the places that short entries
+// leave (nine prompts of up to 8,000 tokens appended and gathered 121 us at 8 deep, 113.5 at 16, 113 at 32, 114.6 at 64).
 unsigned row_grid(const zha_pages* p, int entries, long long items, int per_cta) {
-  long long g = (8LL * p->sms + entries - 1) / entries;
+  long long g = (16LL * p->sms + entries - 1) / entries;
   const long long most = (items + per_cta - 1) / per_cta;
   if (g > most) g = most;
   return (unsigned)(g < 1 ? 1 : g);
