@@ -407,18 +407,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 template <int D, typename TQ, typename TKV>
-cudaError_t launch_fp32(const PrefixArgs& a, cudaStream_t s) {
-  auto kern = fp32_kernel<D, TQ, TKV>;
+cudaError_t launch_fp32(const zha_pages* p, const PrefixArgs& a, cudaStream_t s) {
   const size_t smem = Fp32Tile<D, TQ, TKV>::kSmem;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = allow_shared<fp32_kernel<D, TQ, TKV>>(p, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(a.s.ctas), dim3(kThreads), smem, s, a);
+  return launch_pdl(fp32_kernel<D, TQ, TKV>, dim3(a.s.ctas), dim3(kThreads), smem, s, a);
 }
 
 template <int D>
-cudaError_t launch_fp32_types(const PrefixArgs& a, zha_dtype q, zha_dtype kv, cudaStream_t s) {
-  if (q == ZHA_F32) return kv == ZHA_F32 ? launch_fp32<D, float, float>(a, s) : launch_fp32<D, float, uint16_t>(a, s);
-  return launch_fp32<D, uint16_t, float>(a, s);
+cudaError_t launch_fp32_types(const zha_pages* p, const PrefixArgs& a, zha_dtype q, zha_dtype kv, cudaStream_t s) {
+  if (q == ZHA_F32) return kv == ZHA_F32 ? launch_fp32<D, float, float>(p, a, s) : launch_fp32<D, float, uint16_t>(p, a, s);
+  return launch_fp32<D, uint16_t, float>(p, a, s);
 }
 
 template <int D>
@@ -559,8 +558,8 @@ zha_status zha_prefix_attn_decode(const zha_pages* p, const void* d_Q, zha_dtype
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int d = p->desc.head_dim;
   cudaError_t e = tensor    ? launch_prefix_tc(p, a, d, o_dtype == ZHA_F32, s)
-                  : d == 64 ? launch_fp32_types<64>(a, q_dtype, p->desc.kv_dtype, s)
-                            : launch_fp32_types<128>(a, q_dtype, p->desc.kv_dtype, s);
+                  : d == 64 ? launch_fp32_types<64>(p, a, q_dtype, p->desc.kv_dtype, s)
+                            : launch_fp32_types<128>(p, a, q_dtype, p->desc.kv_dtype, s);
   if (e == cudaSuccess) e = d == 64 ? launch_join<64>(a, o_dtype, s) : launch_join<128>(a, o_dtype, s);
   const_cast<zha_pages*>(p)->launches += 2;  // the handle is logically const
   return e == cudaSuccess ? ZHA_OK : ZHA_ERR_CUDA;

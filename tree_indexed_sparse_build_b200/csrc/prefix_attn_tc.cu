@@ -749,11 +749,10 @@ bool encode(CUtensorMap* map, const void* p, int rank, const cuuint64_t* dims, c
 }
 
 template <int D, bool WIDE>
-cudaError_t launch(const TcArgs& args, cudaStream_t stream) {
-  auto kern = tc_kernel<D, WIDE>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Tc<D>::kSmem);
+cudaError_t launch(const zha_pages* p, const TcArgs& args, cudaStream_t stream) {
+  const cudaError_t e = allow_shared<tc_kernel<D, WIDE>>(p, Tc<D>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(args.a.s.ctas), dim3(kThreads), Tc<D>::kSmem, stream, args);
+  return launch_pdl(tc_kernel<D, WIDE>, dim3(args.a.s.ctas), dim3(kThreads), Tc<D>::kSmem, stream, args);
 }
 
 }  // namespace
@@ -784,8 +783,8 @@ cudaError_t launch_prefix_tc(const zha_pages* p, const PrefixArgs& a, int head_d
   x.a.scale_log2 = fabsf(a.scale_log2);
   // a scale of zero: any size so small that every weight is 1 (0 times a masked score is NaN)
   if (x.a.scale_log2 < 1e-37f) x.a.scale_log2 = 1e-37f;
-  if (head_dim == 64) return wide ? launch<64, true>(x, stream) : launch<64, false>(x, stream);
-  return wide ? launch<128, true>(x, stream) : launch<128, false>(x, stream);
+  if (head_dim == 64) return wide ? launch<64, true>(p, x, stream) : launch<64, false>(p, x, stream);
+  return wide ? launch<128, true>(p, x, stream) : launch<128, false>(p, x, stream);
 }
 
 }  // namespace zha

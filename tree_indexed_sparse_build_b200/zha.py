@@ -170,6 +170,7 @@ def _expect(t: torch.Tensor | None, what: str, numel: int, dtypes: tuple) -> Non
 _I32, _I64, _F32 = (torch.int32,), (torch.int64,), (torch.float32,)
 _OUT = (torch.float32, torch.bfloat16)
 _TORCH_DT = {ZHA_F32: torch.float32, ZHA_BF16: torch.bfloat16}
+_DT_CODE = {t: c for c, t in _TORCH_DT.items()}
 
 
 def zha_tree_get_desc(handle) -> zha_tree_desc:
@@ -466,6 +467,7 @@ class _PagesHandle(ctypes.c_void_p):
     library again at every call would cost a small call a fifth of its time."""
     desc: zha_pages_desc | None = None
     device: int | None = None
+    pool: tuple[torch.dtype, int] | None = None  # type and elements of K, and of V
 
 
 def zha_pages_init(desc: zha_pages_desc, workspace: torch.Tensor, stream=None) -> _PagesHandle:
@@ -473,6 +475,7 @@ def zha_pages_init(desc: zha_pages_desc, workspace: torch.Tensor, stream=None) -
     _check(lib().zha_pages_init(ctypes.byref(desc), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                 _stream(stream), ctypes.byref(h)), "zha_pages_init")
     h.desc, h.device = zha_pages_get_desc(h), zha_pages_device(h)
+    h.pool = _pool_of(h.desc)
     return h
 
 
@@ -516,10 +519,13 @@ def zha_pages_refs(handle) -> int:
     return int(lib().zha_pages_refs(handle) or 0)
 
 
-def _pools(d: zha_pages_desc, *pools, names="KV") -> None:
+def _pool_of(d: zha_pages_desc) -> tuple[torch.dtype, int]:
+    return _TORCH_DT[d.kv_dtype], d.num_pages * d.kv_heads * d.page_tokens * d.head_dim
+
+
+def _pools(handle, *pools, names="KV") -> None:
     """Refuse a pool of another type or size than [num_pages, kv_heads, page_tokens, head_dim]."""
-    n = d.num_pages * d.kv_heads * d.page_tokens * d.head_dim
-    dtype = _TORCH_DT[d.kv_dtype]
+    dtype, n = getattr(handle, "pool", None) or _pool_of(zha_pages_get_desc(handle))
     for name, t in zip(names, pools):
         if t.dtype != dtype:
             raise ValueError(f"{name}: dtype {t.dtype}, the cache's pools are {dtype}")
@@ -590,7 +596,7 @@ def zha_pages_append(handle, K: torch.Tensor, V: torch.Tensor, seqs: torch.Tenso
     """Append K_new, V_new [n, kv_heads, tokens, head_dim] to slots seqs [n]; counts [n]: tokens of
     each entry that count (None: all)."""
     d = zha_pages_get_desc(handle)
-    _pools(d, K, V)
+    _pools(handle, K, V)
     n = _slots(seqs, "seqs")
     T = _rows(d, n, K_new, V_new, "_new")
     _expect(counts, "counts", n, _I32)
@@ -601,7 +607,7 @@ def zha_pages_append(handle, K: torch.Tensor, V: torch.Tensor, seqs: torch.Tenso
 def zha_pages_fork(handle, K: torch.Tensor, V: torch.Tensor, src: torch.Tensor, dst: torch.Tensor,
                    stream=None) -> None:
     """Empty slots dst [n] become forks of sequences src [n]."""
-    _pools(zha_pages_get_desc(handle), K, V)
+    _pools(handle, K, V)
     n = _slots(src, "src")
     _slots(dst, "dst", n)
     _check(lib().zha_pages_fork(handle, *_on(handle, K, V, src, dst), n, _raw_stream(handle, stream)),
@@ -611,8 +617,8 @@ def zha_pages_fork(handle, K: torch.Tensor, V: torch.Tensor, src: torch.Tensor, 
 def zha_pages_copy(from_handle, K_from: torch.Tensor, V_from: torch.Tensor, handle, K: torch.Tensor,
                    V: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
     """Empty slots dst [n] become copies of sequences src [n] of the cache from_handle."""
-    _pools(zha_pages_get_desc(from_handle), K_from, V_from, names=("K_from", "V_from"))
-    _pools(zha_pages_get_desc(handle), K, V)
+    _pools(from_handle, K_from, V_from, names=("K_from", "V_from"))
+    _pools(handle, K, V)
     n = _slots(src, "src")
     _slots(dst, "dst", n)
     kf, vf, k, v, a, b = _on(handle, K_from, V_from, K, V, src, dst)
@@ -628,7 +634,7 @@ def zha_pages_free(handle, seqs: torch.Tensor, stream=None) -> None:
 def zha_pages_compact(handle, K: torch.Tensor, V: torch.Tensor, live: torch.Tensor | None = None,
                       stream=None) -> None:
     """Move the pages in use to the bottom of the pools; live [1] receives how many there are."""
-    _pools(zha_pages_get_desc(handle), K, V)
+    _pools(handle, K, V)
     _expect(live, "live", 1, _I32)
     _check(lib().zha_pages_compact(handle, *_on(handle, K, V, live), _raw_stream(handle, stream)), "zha_pages_compact")
 
@@ -637,7 +643,7 @@ def zha_pages_gather(handle, K: torch.Tensor, V: torch.Tensor, seqs: torch.Tenso
                      V_out: torch.Tensor, stream=None) -> None:
     """Copy sequences seqs [n] into a dense cache [n, kv_heads, capacity, head_dim]."""
     d = zha_pages_get_desc(handle)
-    _pools(d, K, V)
+    _pools(handle, K, V)
     n = _slots(seqs, "seqs")
     cap = _rows(d, n, K_out, V_out, "_out")
     k, v, s, ko, vo = _on(handle, K, V, seqs, K_out, V_out)
@@ -656,18 +662,20 @@ def zha_prefix_attn_decode(handle, Q: torch.Tensor, K: torch.Tensor, V: torch.Te
                            prefix_seq: int, prefix_tokens: int, causal: bool, scale: float, O: torch.Tensor,
                            scratch: torch.Tensor, stream=None) -> None:
     """Attention of slots seqs [batch] whose first prefix_tokens tokens are prefix_seq's pages."""
-    d = zha_pages_get_desc(handle)
-    if Q.dim() != 4 or Q.shape[3] != d.head_dim:
-        raise ValueError(f"Q: shape {tuple(Q.shape)}, expected [batch, q_heads, nq, {d.head_dim}]")
-    B, Hq, nq, _ = Q.shape
-    _expect(Q, "Q", Q.numel(), _OUT)
-    _expect(O, "O", Q.numel(), _OUT)
-    _pools(d, K, V)
+    shape = Q.shape
+    d = zha_pages_get_desc(handle).head_dim
+    if len(shape) != 4 or shape[3] != d:
+        raise ValueError(f"Q: shape {tuple(shape)}, expected [batch, q_heads, nq, {d}]")
+    B, Hq, nq, _ = shape
+    qt, ot, n = _DT_CODE.get(Q.dtype), _DT_CODE.get(O.dtype), Q.numel()
+    if qt is None or ot is None or O.numel() != n:
+        _expect(Q, "Q", n, _OUT)
+        _expect(O, "O", n, _OUT)
+    _pools(handle, K, V)
     _slots(seqs, "seqs", B)
     q, k, v, s, o, x = _on(handle, Q, K, V, seqs, O, scratch)
-    _check(lib().zha_prefix_attn_decode(handle, q, dtype_code(Q.dtype), B, Hq, nq, k, v, s, prefix_seq, prefix_tokens,
-                                        int(causal), scale, o, dtype_code(O.dtype), x,
-                                        scratch.numel() * scratch.element_size(), _raw_stream(handle, stream)),
+    _check(lib().zha_prefix_attn_decode(handle, q, qt, B, Hq, nq, k, v, s, prefix_seq, prefix_tokens, int(causal), scale,
+                                        o, ot, x, scratch.nbytes, _raw_stream(handle, stream)),
            "zha_prefix_attn_decode")
 
 
@@ -948,17 +956,17 @@ class Pages:
                out_dtype: torch.dtype = torch.bfloat16, O: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """Attention of Q [batch, q_heads, nq, head_dim] over slots seqs [batch], whose first
         prefix_tokens tokens are the pages of slot prefix_seq."""
-        if Q.dim() != 4:
-            raise ValueError(f"Q: shape {tuple(Q.shape)}, expected [batch, q_heads, nq, {self.desc.head_dim}]")
-        B, Hq, nq, _ = Q.shape
-        need = lib().zha_prefix_attn_scratch_bytes(self.handle, B, Hq, nq, prefix_tokens)
+        shape = Q.shape
+        if len(shape) != 4:
+            raise ValueError(f"Q: shape {tuple(shape)}, expected [batch, q_heads, nq, {self.desc.head_dim}]")
+        need = lib().zha_prefix_attn_scratch_bytes(self.handle, shape[0], shape[1], shape[2], prefix_tokens) + 16
         if stream is None:  # (the usual call, without the context's 2 us)
-            O = Q.new_empty(Q.shape, dtype=out_dtype) if O is None else O
-            scratch = Q.new_empty((need + 16,), dtype=torch.uint8)
+            O = Q.new_empty(shape, dtype=out_dtype) if O is None else O
+            scratch = Q.new_empty(need, dtype=torch.uint8)
         else:
             with _allocating(stream):
-                O = Q.new_empty(Q.shape, dtype=out_dtype) if O is None else O
-                scratch = Q.new_empty((need + 16,), dtype=torch.uint8)
+                O = Q.new_empty(shape, dtype=out_dtype) if O is None else O
+                scratch = Q.new_empty(need, dtype=torch.uint8)
         zha_prefix_attn_decode(self.handle, Q, K, V, seqs, prefix_seq, prefix_tokens, causal, scale, O, scratch, stream)
         return O
 
