@@ -153,6 +153,48 @@ def test_growing_maximum(types):
     _compare(got, Q, K, V, table, [512, 1500], [0, 1], 1.0, 0, 512, False, kv, q, out)
 
 
+@pytest.mark.parametrize("types", TYPES[:3], ids=lambda t: "-".join(str(x)[6:] for x in t))
+@pytest.mark.parametrize("step", [0.05, 1.0])
+def test_maximum_that_grows_over_many_tiles(types, step):
+    # rows whose scores rise (and fall) by up to a hundred and more within the tiles of one sum
+    zha = _zha()
+    kv, q, out = types
+    n = [6000, 2111]
+    pages, Q, K, V, table = _case(zha, 1, 4, 64, 16, 0, n, 2, kv, q)
+    for s in range(2):
+        for j in range(-(-n[s] // 16)):
+            r = min(16, n[s] - 16 * j)
+            K[int(table[s, j]), :, :r] = (K[int(table[s, j]), :, :r].float() * 0.1 + step * j).to(kv)
+    got = pages.attend(Q.cuda(), K.cuda(), V.cuda(), 0.125, _i32([0, 1]), out_dtype=out)
+    assert pages.check() == zha.ZHA_OK
+    _compare(got, Q, K, V, table, n, [0, 1], 0.125, 0, 0, False, kv, q, out)
+
+
+def test_long_sums_of_an_fp32_output_do_not_shrink():
+    # The tensor core cuts its sums off: up to 2^-23 of a sum at each product, half of that on average.  A sum takes at most
+    # 96 products before it is added in fp32, so outputs are short by no more than 96 * 2^-24 = 5.7e-6 on average (the
+    # sums of every CTA here would take 1,600 products and more).
+    zha = _zha()
+    heads, group, d, page, prefix, batch, nq = 8, 8, 128, 64, 32768, 40, 4
+    lens = [prefix] * batch
+    gen = torch.Generator().manual_seed(3)
+    K, V = (torch.randn((prefix // page, heads, page, d), generator=gen).to(BF16).cuda() for _ in "KV")
+    Q = torch.randn((batch, heads * group, nq, d), generator=gen).to(BF16).cuda()
+    pages = zha.Pages(heads, d, page, prefix // page, batch, prefix // page, BF16)
+    pages.load(torch.arange(prefix // page, dtype=torch.int32, device="cuda").repeat(batch, 1), _i32(lens))
+    got = pages.attend(Q, K, V, d ** -0.5, _i32(list(range(batch))), 0, prefix, False, F32)
+    assert pages.check() == zha.ZHA_OK
+    short, size = 0.0, 0.0
+    for h in range(heads):
+        q = Q[:, h * group:(h + 1) * group].reshape(-1, d).double()
+        k, v = (x[:, h].reshape(-1, d).double() for x in (K, V))
+        o = torch.softmax(q @ k.T * d ** -0.5, -1) @ v
+        x = got[:, h * group:(h + 1) * group].reshape(-1, d).double()
+        short += float(((o - x) * o).sum())
+        size += float((o * o).sum())
+    assert abs(short / size) <= 96 * 2.0 ** -24
+
+
 @pytest.mark.parametrize("own", [1, 200])
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 @pytest.mark.parametrize("types", TYPES, ids=lambda t: "-".join(str(x)[6:] for x in t))

@@ -24,13 +24,6 @@
 // rescaled.  Rows of a page past the sequence may hold anything: their scores are replaced, and
 // the rows of V that an MMA step still touches are zeroed in shared memory, because 0 times NaN is NaN.
 //
-// Bound: a pair of dual tiles takes 3,900 clocks, 2,048 of them tensor work; the rest is the chain from scores to weights
-// (2,000) to product, which two streams hide in part.  Measured with the join, 32 query and 8 KV heads of 128: 64
-// sequences on a prefix of 131,072 tokens 207 us (0.67 PFLOP/s, 3.2 TB/s), 33 sequences of up to 4,000 tokens, nothing
-// shared, 61 us (4.5 TB/s), eight sequences of four queries on 32,768 tokens, fp32 output, 59 us; with 64 query heads 16
-// sequences on 1,048,576 tokens 756 us (5.7 TB/s).
-// Twice the warps for the weights (16 rows each, 96 registers a thread) spilled and took 229 us for the first of these.
-//
 // Every wait is bounded; one that runs out sets an error that makes all warps leave, the
 // producer waiting (bounded) for its loads and the issuer for its MMAs.
 #include <cmath>
@@ -46,6 +39,12 @@ constexpr int kRows = 128;
 // Keys of a tile.  An fp32 output wants the weights in 24 bits: three bf16 numbers each, whose three MMAs with V
 // find room in S only for 64 keys.  (Two numbers for 128 keys were off by 1.5e-6 of the output.)
 __host__ __device__ constexpr int keys_of(bool wide) { return wide ? 64 : 128; }
+// Tiles whose products with V one sum in TMEM takes before it is added (in fp32, rounded) to the partial result in
+// memory.  The tensor core cuts its sums off instead of rounding them: at each of the 12 MMAs of a tile with an fp32 output
+// they lose 1.6e-8 of themselves on average.  Without end, an output over 120,000 tokens was off by 2.1e-5; with 16 tiles a
+// sum 3.5e-6, with 8 1.8e-6, with 4 1.0e-6, for 61, 61, 65 and 71 us of eight sequences of four queries on 32,768 tokens.
+// (A bf16 output's sums may lose 1e-4 on their way through a share of 1,000 tiles, a twentieth of its weights' rounding.)
+__host__ __device__ constexpr int tiles_per_sum(bool wide) { return wide ? 8 : 1 << 30; }
 constexpr int kThreads = 384;
 constexpr int kTmemCols = 512;
 constexpr int kByFma = 2;     // of 16 pairs of weights, those whose exp2 the FMA pipes compute
@@ -62,6 +61,11 @@ struct TcArgs {
   int chunk, chunk_shift;           // rows a page contributes to a key tile
   int flip;                         // scale < 0: scores are negated and a.scale_log2 is its size
 };
+
+// Adds two values in memory.  (Whoever adds is the only one, so the order of the sums is the program's.)
+__device__ __forceinline__ void add_to(float* p, float x, float y) {
+  asm volatile("red.relaxed.gpu.global.add.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(x), "f"(y) : "memory");
+}
 
 template <int D>
 struct Tc {
@@ -83,7 +87,7 @@ static_assert(sizeof(Bars) <= 1024, "the barriers' page");
 
 // What the issuers have to know of a tile, written by the loaders.
 enum TileFlags {
-  kFirst = 1,   // its stream's first tile of the segment
+  kFirst = 1,   // keys: its stream's first tile of the segment; values: of a sum
   kLast = 2,    // .. last
   kPaired = 4,  // a dual tile: both streams'
   kAlone = 8,   // keys: one stream alone uses the queries
@@ -160,7 +164,7 @@ constexpr int kStreamRegs = 192, kOtherRegs = 120;
 
 // ---- warps 8 and 9
 
-template <int D>
+template <int D, bool WIDE>
 struct Loader {
   using C = Tc<D>;
   const TcArgs& args;
@@ -234,8 +238,10 @@ struct Loader {
       const Segment g = x.g;
       const bool with_queries = KEYS && x.t == x.g.t0;
       int flags = dual ? kPaired : 0;
-      if (x.t < x.g.t0 + by) flags |= kFirst;
-      if (x.t + by >= x.g.t1) flags |= kLast;
+      const bool sums = !KEYS && WIDE;  // first and last of a sum, else of the segment
+      const int j = (x.t - x.g.t0) >> (by - 1);
+      if (sums ? j % tiles_per_sum(WIDE) == 0 : j == 0) flags |= kFirst;
+      if (x.t + by >= x.g.t1 || (sums && (j + 1) % tiles_per_sum(WIDE) == 0)) flags |= kLast;
       if (KEYS) {
         if (dual || x.g.t1 - x.g.t0 == 1) flags |= kAlone;
         flags |= ((with_queries ? qc : qc - 1 - dual) & 3) * kQuery;
@@ -459,8 +465,9 @@ struct Stream {
       fix = exp2_approx(m - top);
       m = top;
     }
+    if (WIDE) l *= fix;  // (a fresh sum may follow another)
     if (!fresh && __any_sync(0xffffffffu, fix != 1.f)) {
-      l *= fix;
+      if (!WIDE) l *= fix;
 #pragma unroll
       for (int q = 0; q < D / 16; ++q) {
         uint32_t y[16];
@@ -525,6 +532,20 @@ struct Stream {
       }
   }
 
+  // A sum in memory, times a factor of each lane's row.
+  __device__ __noinline__ void rescale(size_t slot, bool valid, float by) {
+    __threadfence();
+    __syncwarp();
+    for (int r = 0; r < 32; ++r) {
+      const float f = __shfl_sync(0xffffffffu, by, r);
+      if (!__shfl_sync(0xffffffffu, valid, r)) continue;
+      float* p = a.acc + (slot + r) * D;
+      for (int c = lane; c < D; c += 32) __stcg(p + c, __ldcg(p + c) * f);
+    }
+    __threadfence();
+    __syncwarp();
+  }
+
   // This stream's tiles j0, j0 + by, .. of a segment that starts with the share's tile `tile0`.
   __device__ __forceinline__ bool segment(const Segment& g, int j0, int by, uint32_t tile0) {
     constexpr int kKeys = keys_of(WIDE), kQuarter = kKeys / 4;
@@ -563,7 +584,11 @@ struct Stream {
     const bool work = __any_sync(0xffffffffu, valid);
     m = -INFINITY;
     l = 0.f;
-    for (int j = j0; j < n; j += by) {
+    float put_m = -INFINITY;  // WIDE: the maximum that the sums in memory refer to
+    int j = j0;
+  again:
+    const int sum0 = j, sum1 = WIDE ? min(n, j + tiles_per_sum(WIDE) * by) : n;  // the tiles of one sum
+    for (; j < sum1; j += by) {
       const int k0 = first + (g.t0 + j) * kKeys, left = min(kKeys, g.len - k0);  // first key, keys
       if (!wait(&bars.s_full[st], ns++ & 1)) return false;
       tc_fence_after();
@@ -582,11 +607,11 @@ struct Stream {
       }
       if (work) {
         if (parts == 4) {
-          weigh<kQuarter>(kQuarter * quarter, row_end - k0 - kQuarter * quarter, j == j0);
+          weigh<kQuarter>(kQuarter * quarter, row_end - k0 - kQuarter * quarter, j == sum0);
           __syncwarp();
           clear_others();
         } else {
-          weigh<kKeys>(0, row_end - k0, j == j0);
+          weigh<kKeys>(0, row_end - k0, j == sum0);
         }
         tmem_wait_st();
       }
@@ -599,19 +624,37 @@ struct Stream {
     if (work) {
       const int part = g.kind == kDual ? st : (j0 * parts + (parts == 4 ? quarter : 0));
       const size_t slot = (size_t)g.slot + part * rows + (parts == 4 ? 0 : quarter * 32);  // of this warp's first row
-      if (valid) a.ml[slot + lane] = make_float2(m, l);
+      float fix = 1.f;  // WIDE: from what this sum's weights refer to, to what the sums in memory do
+      if (WIDE) {
+        if (sum0 == j0) put_m = m;
+        if (__any_sync(0xffffffffu, m != put_m && !(m <= put_m + 60.f))) {  // (what is there is nothing next to this sum)
+          rescale(slot, valid, put_m == -INFINITY ? 0.f : exp2_approx(put_m - m));
+          put_m = m;
+        }
+        if (m != put_m) fix = exp2_approx(m - put_m);
+      }
+      if (valid) a.ml[slot + lane] = WIDE ? make_float2(put_m, l * fix) : make_float2(m, l);
       // in whole 32-byte sectors: a row a thread, 16 bytes at a time, took four times as long (13,000 clocks)
       const unsigned some = __ballot_sync(0xffffffffu, valid);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (!(some >> (16 * i) & 0xffffu)) continue;
         const int r0 = 16 * i + lane / 4;
+        const float f0 = WIDE ? __shfl_sync(0xffffffffu, fix, r0) : 0.f, f1 = WIDE ? __shfl_sync(0xffffffffu, fix, r0 + 8) : 0.f;
         float* out = a.acc + (slot + r0) * D + lane % 4 * 2;
 #pragma unroll
         for (int c = 0; c < D; c += 64) {
           uint32_t y[32];
           tmem_ld_blocks(y, to + (16u * i << 16) + c);
           tmem_wait_ld();
+          if (WIDE && sum0 > j0) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (some >> (r0 + k % 2 * 8) & 1)
+                add_to(out + k % 2 * 8 * D + c + k / 2 * 8, __uint_as_float(y[2 * k]) * (k & 1 ? f1 : f0),
+                       __uint_as_float(y[2 * k + 1]) * (k & 1 ? f1 : f0));
+            continue;
+          }
           if (some >> r0 & 1) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) *reinterpret_cast<uint2*>(out + c + 8 * k) = make_uint2(y[4 * k], y[4 * k + 1]);
@@ -627,6 +670,7 @@ struct Stream {
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars.o_free[st]);
+    if (WIDE && j < n) goto again;
     return true;
   }
 
@@ -693,10 +737,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
   } else {
     fewer_registers<kOtherRegs>();
     if (warp == 8) {
-      Loader<D> x(args, bars, wait, q_smem, q_smem + 2 * C::kTile);
+      Loader<D, WIDE> x(args, bars, wait, q_smem, q_smem + 2 * C::kTile);
       if (!x.template run<true>(walk, cta)) x.template drain<true>();
     } else if (warp == 9) {
-      Loader<D> x(args, bars, wait, q_smem, q_smem + (2 + C::kKStages) * C::kTile);
+      Loader<D, WIDE> x(args, bars, wait, q_smem, q_smem + (2 + C::kKStages) * C::kTile);
       if (!x.template run<false>(walk, cta)) x.template drain<false>();
     } else {
       Issuer<D, WIDE> x(args, bars, wait, q_smem, tmem, warp - 10);
@@ -749,10 +793,11 @@ bool encode(CUtensorMap* map, const void* p, int rank, const cuuint64_t* dims, c
 }
 
 template <int D, bool WIDE>
-cudaError_t launch(const zha_pages* p, const TcArgs& args, cudaStream_t stream) {
-  const cudaError_t e = allow_shared<tc_kernel<D, WIDE>>(p, Tc<D>::kSmem);
+cudaError_t launch(const TcArgs& args, cudaStream_t stream) {
+  auto kern = tc_kernel<D, WIDE>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Tc<D>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(tc_kernel<D, WIDE>, dim3(args.a.s.ctas), dim3(kThreads), Tc<D>::kSmem, stream, args);
+  return launch_pdl(kern, dim3(args.a.s.ctas), dim3(kThreads), Tc<D>::kSmem, stream, args);
 }
 
 }  // namespace
@@ -783,8 +828,8 @@ cudaError_t launch_prefix_tc(const zha_pages* p, const PrefixArgs& a, int head_d
   x.a.scale_log2 = fabsf(a.scale_log2);
   // a scale of zero: any size so small that every weight is 1 (0 times a masked score is NaN)
   if (x.a.scale_log2 < 1e-37f) x.a.scale_log2 = 1e-37f;
-  if (head_dim == 64) return wide ? launch<64, true>(p, x, stream) : launch<64, false>(p, x, stream);
-  return wide ? launch<128, true>(p, x, stream) : launch<128, false>(p, x, stream);
+  if (head_dim == 64) return wide ? launch<64, true>(x, stream) : launch<64, false>(x, stream);
+  return wide ? launch<128, true>(x, stream) : launch<128, false>(x, stream);
 }
 
 }  // namespace zha
