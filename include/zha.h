@@ -400,6 +400,7 @@ zha_status zha_pages_gather(const zha_pages* pages, const void* d_K, const void*
  * Rows of the pools that hold no token are never used, whatever they contain.  A slot out of range
  * counts as an empty sequence, a page id out of range as a page of zeros; those, and a prefix longer than
  * prefix_seq, set ZHA_ERR_DEVICE.  Values of tokens that any query of a call sees must be finite.
+ * A score that is NaN or +infinity makes its query's output NaN and no other's.
  * bf16 queries over a bf16 cache run on the tensor cores: products are exact, sums fp32; for a bf16 output
  * the softmax weights are rounded to bf16 before they meet V, for an fp32 output they keep 24 bits.
  * All other types run in fp32. */
