@@ -21,6 +21,13 @@ torch = pytest.importorskip("torch")
 BF16, F32 = torch.bfloat16, torch.float32
 
 
+@pytest.fixture(scope="module", autouse=True)
+def _give_memory_back():
+    yield  # the largest pools here hold several GB
+    if torch.cuda.is_available():
+        torch.cuda.empty_cache()
+
+
 def _zha():
     if not torch.cuda.is_available():
         pytest.skip("needs a GPU")

@@ -586,91 +586,92 @@ struct Stream {
     l = 0.f;
     float put_m = -INFINITY;  // WIDE: the maximum that the sums in memory refer to
     int j = j0;
-  again:
-    const int sum0 = j, sum1 = WIDE ? min(n, j + tiles_per_sum(WIDE) * by) : n;  // the tiles of one sum
-    for (; j < sum1; j += by) {
-      const int k0 = first + (g.t0 + j) * kKeys, left = min(kKeys, g.len - k0);  // first key, keys
-      if (!wait(&bars.s_full[st], ns++ & 1)) return false;
-      tc_fence_after();
-      if (left & 15) {  // rows of V behind the sequence, up to the end of the last MMA's 16
-        const uint32_t p = tile0 + j;
-        const int stage = p % C::kVStages;
-        if (!wait(&bars.v_full[stage], (p / C::kVStages) & 1)) return false;
-        if (r >= left && r < ((left + 15) & ~15)) {
-          char* v = ring + stage * C::kTile + r * 128;
+    do {
+      const int sum0 = j, sum1 = WIDE ? min(n, j + tiles_per_sum(WIDE) * by) : n;  // the tiles of one sum
+      for (; j < sum1; j += by) {
+        const int k0 = first + (g.t0 + j) * kKeys, left = min(kKeys, g.len - k0);  // first key, keys
+        if (!wait(&bars.s_full[st], ns++ & 1)) return false;
+        tc_fence_after();
+        if (left & 15) {  // rows of V behind the sequence, up to the end of the last MMA's 16
+          const uint32_t p = tile0 + j;
+          const int stage = p % C::kVStages;
+          if (!wait(&bars.v_full[stage], (p / C::kVStages) & 1)) return false;
+          if (r >= left && r < ((left + 15) & ~15)) {
+            char* v = ring + stage * C::kTile + r * 128;
 #pragma unroll
-          for (int x = 0; x < D / 64; ++x)
+            for (int x = 0; x < D / 64; ++x)
 #pragma unroll
-            for (int y = 0; y < 8; ++y) *reinterpret_cast<uint4*>(v + x * C::kHalf + y * 16) = make_uint4(0, 0, 0, 0);
+              for (int y = 0; y < 8; ++y) *reinterpret_cast<uint4*>(v + x * C::kHalf + y * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
         }
-        fence_proxy_async_smem();
+        if (work) {
+          if (parts == 4) {
+            weigh<kQuarter>(kQuarter * quarter, row_end - k0 - kQuarter * quarter, j == sum0);
+            __syncwarp();
+            clear_others();
+          } else {
+            weigh<kKeys>(0, row_end - k0, j == sum0);
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_ready[st]);
       }
+      if (!wait(&bars.o_full[st], no++ & 1)) return false;
+      tc_fence_after();
       if (work) {
-        if (parts == 4) {
-          weigh<kQuarter>(kQuarter * quarter, row_end - k0 - kQuarter * quarter, j == sum0);
-          __syncwarp();
-          clear_others();
-        } else {
-          weigh<kKeys>(0, row_end - k0, j == sum0);
+        const int part = g.kind == kDual ? st : (j0 * parts + (parts == 4 ? quarter : 0));
+        const size_t slot = (size_t)g.slot + part * rows + (parts == 4 ? 0 : quarter * 32);  // of this warp's first row
+        float fix = 1.f;  // WIDE: from what this sum's weights refer to, to what the sums in memory do
+        if (WIDE) {
+          if (sum0 == j0) put_m = m;
+          // (up to 2^16 this sum is scaled, which leaves it finite; more is rare, and what is there is scaled)
+          if (__any_sync(0xffffffffu, m != put_m && !(m <= put_m + 2 * kSlack))) {
+            rescale(slot, valid, put_m == -INFINITY ? 0.f : exp2_approx(put_m - m));
+            put_m = m;
+          }
+          if (m != put_m) fix = exp2_approx(m - put_m);
         }
-        tmem_wait_st();
+        if (valid) a.ml[slot + lane] = WIDE ? make_float2(put_m, l * fix) : make_float2(m, l);
+        // in whole 32-byte sectors: a row a thread, 16 bytes at a time, took four times as long (13,000 clocks)
+        const unsigned some = __ballot_sync(0xffffffffu, valid);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (!(some >> (16 * i) & 0xffffu)) continue;
+          const int r0 = 16 * i + lane / 4;
+          const float f0 = WIDE ? __shfl_sync(0xffffffffu, fix, r0) : 0.f, f1 = WIDE ? __shfl_sync(0xffffffffu, fix, r0 + 8) : 0.f;
+          float* out = a.acc + (slot + r0) * D + lane % 4 * 2;
+#pragma unroll
+          for (int c = 0; c < D; c += 64) {
+            uint32_t y[32];
+            tmem_ld_blocks(y, to + (16u * i << 16) + c);
+            tmem_wait_ld();
+            if (WIDE && sum0 > j0) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                if (some >> (r0 + k % 2 * 8) & 1)
+                  add_to(out + k % 2 * 8 * D + c + k / 2 * 8, __uint_as_float(y[2 * k]) * (k & 1 ? f1 : f0),
+                         __uint_as_float(y[2 * k + 1]) * (k & 1 ? f1 : f0));
+              continue;
+            }
+            if (some >> r0 & 1) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) *reinterpret_cast<uint2*>(out + c + 8 * k) = make_uint2(y[4 * k], y[4 * k + 1]);
+            }
+            if (some >> (r0 + 8) & 1) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<uint2*>(out + 8 * D + c + 8 * k) = make_uint2(y[4 * k + 2], y[4 * k + 3]);
+            }
+          }
+        }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.p_ready[st]);
-    }
-    if (!wait(&bars.o_full[st], no++ & 1)) return false;
-    tc_fence_after();
-    if (work) {
-      const int part = g.kind == kDual ? st : (j0 * parts + (parts == 4 ? quarter : 0));
-      const size_t slot = (size_t)g.slot + part * rows + (parts == 4 ? 0 : quarter * 32);  // of this warp's first row
-      float fix = 1.f;  // WIDE: from what this sum's weights refer to, to what the sums in memory do
-      if (WIDE) {
-        if (sum0 == j0) put_m = m;
-        if (__any_sync(0xffffffffu, m != put_m && !(m <= put_m + 60.f))) {  // (what is there is nothing next to this sum)
-          rescale(slot, valid, put_m == -INFINITY ? 0.f : exp2_approx(put_m - m));
-          put_m = m;
-        }
-        if (m != put_m) fix = exp2_approx(m - put_m);
-      }
-      if (valid) a.ml[slot + lane] = WIDE ? make_float2(put_m, l * fix) : make_float2(m, l);
-      // in whole 32-byte sectors: a row a thread, 16 bytes at a time, took four times as long (13,000 clocks)
-      const unsigned some = __ballot_sync(0xffffffffu, valid);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (!(some >> (16 * i) & 0xffffu)) continue;
-        const int r0 = 16 * i + lane / 4;
-        const float f0 = WIDE ? __shfl_sync(0xffffffffu, fix, r0) : 0.f, f1 = WIDE ? __shfl_sync(0xffffffffu, fix, r0 + 8) : 0.f;
-        float* out = a.acc + (slot + r0) * D + lane % 4 * 2;
-#pragma unroll
-        for (int c = 0; c < D; c += 64) {
-          uint32_t y[32];
-          tmem_ld_blocks(y, to + (16u * i << 16) + c);
-          tmem_wait_ld();
-          if (WIDE && sum0 > j0) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (some >> (r0 + k % 2 * 8) & 1)
-                add_to(out + k % 2 * 8 * D + c + k / 2 * 8, __uint_as_float(y[2 * k]) * (k & 1 ? f1 : f0),
-                       __uint_as_float(y[2 * k + 1]) * (k & 1 ? f1 : f0));
-            continue;
-          }
-          if (some >> r0 & 1) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) *reinterpret_cast<uint2*>(out + c + 8 * k) = make_uint2(y[4 * k], y[4 * k + 1]);
-          }
-          if (some >> (r0 + 8) & 1) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<uint2*>(out + 8 * D + c + 8 * k) = make_uint2(y[4 * k + 2], y[4 * k + 3]);
-          }
-        }
-      }
-    }
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bars.o_free[st]);
-    if (WIDE && j < n) goto again;
+      if (lane == 0) mbar_arrive(&bars.o_free[st]);
+    } while (WIDE && j < n);
     return true;
   }
 
