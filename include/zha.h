@@ -395,12 +395,18 @@ zha_status zha_pages_gather(const zha_pages* pages, const void* d_K, const void*
  *                  len - nq + i and sees the tokens up to itself.  A query that sees no token gives zeros
  *   scale          multiplies q . k before the softmax; finite
  *   d_O            out [batch, q_heads, nq, head_dim] in o_dtype
- *   d_scratch      >= zha_prefix_attn_scratch_bytes(pages, batch, q_heads, nq, prefix_tokens) bytes,
- *                  16-byte aligned; contents need no initialisation.  Calls that may overlap need one each
+ *   d_scratch      >= zha_prefix_attn_scratch_bytes(pages, batch, q_heads, nq, prefix_tokens) bytes (enough for the
+ *                  types that these sizes are supported for, 0 when there are none; a call with less than it
+ *                  needs is ZHA_ERR_INVALID_ARG), 16-byte aligned; contents need no initialisation.  Calls that may
+ *                  overlap need one each
  * Rows of the pools that hold no token are never used, whatever they contain.  A slot out of range
  * counts as an empty sequence, a page id out of range as a page of zeros; those, and a prefix longer than
  * prefix_seq, set ZHA_ERR_DEVICE.  Values of tokens that any query of a call sees must be finite.
  * A score that is NaN or +infinity makes its query's output NaN and no other's.
+ * ZHA_ERR_UNSUPPORTED where an index would not fit: rows = q_heads / kv_heads * nq > 2^20, batch > 2^20, batch *
+ * kv_heads * rows > 2^30, or 2^31 tiles of work, counted for sequences of max_seq_pages pages: of 128 rows and
+ * 128 keys (64 for an fp32 output) for bf16 queries over a bf16 cache, of 64 rows (16, where a sequence has no more) and 32
+ * keys for other types.
  * bf16 queries over a bf16 cache run on the tensor cores: products are exact, sums fp32; for a bf16 output
  * the softmax weights are rounded to bf16 before they meet V, for an fp32 output they keep 24 bits.
  * All other types run in fp32. */

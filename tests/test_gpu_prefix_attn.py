@@ -528,3 +528,23 @@ def test_nothing_to_do():
     assert pages.attend(Q[:0].cuda(), K.cuda(), V.cuda(), 0.1, _i32([])).shape == (0, 1, 1, 64)
     assert pages.attend(Q[:, :, :0].contiguous().cuda(), K.cuda(), V.cuda(), 0.1, _i32([0])).shape == (1, 1, 0, 64)
     assert pages.launches == before
+
+
+def test_scratch_of_a_call_that_only_bf16_queries_fit():
+    # 128 entries of up to 16,777,216 tokens on 32 heads: more than 2^31 tiles of 32 keys, a quarter as many of 128
+    zha = _zha()
+    heads, d, page, batch = 32, 128, 256, 128
+    pages, Q, K, V, table = _case(zha, heads, 1, d, page, 0, [300], 1, BF16, BF16, width=65536)
+    q, k, v, seqs = Q.repeat(batch, 1, 1, 1).cuda(), K.cuda(), V.cuda(), _i32([0] * batch)
+    for out in (BF16, F32):
+        O = torch.full(q.shape, 7.0, dtype=out, device="cuda")
+        with pytest.raises(zha.ZhaError) as e:
+            zha.zha_prefix_attn_decode(pages.handle, q, k, v, seqs, 0, 0, False, 0.1, O,
+                                       torch.zeros(16, dtype=torch.uint8, device="cuda"))
+        assert e.value.status == zha.ZHA_ERR_INVALID_ARG and (O == 7).all()
+        got = pages.attend(q, k, v, 0.1, seqs, out_dtype=out)
+        assert pages.check() == zha.ZHA_OK
+        _compare(got, q.cpu(), K, V, table, [300], [0] * batch, 0.1, 0, 0, False, BF16, BF16, out)
+    with pytest.raises(zha.ZhaError) as e:
+        pages.attend(q.float(), k, v, 0.1, seqs)
+    assert e.value.status == zha.ZHA_ERR_UNSUPPORTED

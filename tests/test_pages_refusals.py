@@ -154,3 +154,26 @@ def test_what_fits_reaches_the_device_check():
                  lambda: zha.zha_prefix_attn_decode(H, _new(), K, V, _s(), 0, 0, False, 0.1, _new(), _s())):
         with pytest.raises(ValueError, match="device tensors"):
             call()
+
+
+def _handle(**kw):
+    """Memory that looks like a handle of this geometry on a device that is not there (all of its other
+    fields are 148): for what a call answers before it asks the device."""
+    d = _desc(**kw)
+    h = (ctypes.c_int * 256)(*[148] * 256)
+    ctypes.memmove(h, ctypes.byref(d), ctypes.sizeof(d))
+    assert zha.lib().zha_pages_device(h) == 148
+    return h
+
+
+@pytest.mark.parametrize("geometry,q_heads,nq,batches", [
+    # (32-key tiles of fp32 queries pass 31 bits between the two batches, 128-key tiles of bf16 queries do not)
+    (dict(kv_heads=32, head_dim=128, page_tokens=256, num_pages=4, max_seqs=1, max_seq_pages=65536), 32, 1, (127, 128)),
+    (dict(kv_heads=8, head_dim=128, page_tokens=64, num_pages=4, max_seqs=1, max_seq_pages=16384), 64, 512, (15, 128))])
+def test_scratch_of_a_call_that_only_some_types_fit(geometry, q_heads, nq, batches):
+    size = zha.lib().zha_prefix_attn_scratch_bytes
+    h = _handle(**geometry)
+    few, many = (size(h, b, q_heads, nq, 0) for b in batches)
+    # a row's maximum, sum and head_dim values, for every row at least
+    assert many >= batches[1] * q_heads * nq * (geometry["head_dim"] + 2) * 4 and few >= many * batches[0] // batches[1] // 2
+    assert size(h, 2 ** 20 + 1, q_heads, nq, 0) == 0 and size(h, 1, q_heads, 2 ** 20 + 1, 0) == 0

@@ -510,9 +510,9 @@ size_t zha_prefix_attn_scratch_bytes(const zha_pages* p, int batch, int q_heads,
   if (!p || prefix_tokens < 0 || prefix_tokens > 1LL << 30) return 0;
   PrefixShape s;
   size_t most = 0;
-  for (int kind = 0; kind < 3; ++kind) {  // whatever the queries' and the output's type
+  for (int kind = 0; kind < 3; ++kind) {  // whatever the queries' and the output's type, if they can be planned
     if (kind && p->desc.kv_dtype != ZHA_BF16) break;
-    if (!plan(p, batch, q_heads, nq, prefix_tokens, kind > 0, kind > 1, &s)) return 0;
+    if (!plan(p, batch, q_heads, nq, prefix_tokens, kind > 0, kind > 1, &s)) continue;
     const size_t n = scratch_of(p, s).bytes;
     if (n > most) most = n;
   }
@@ -539,8 +539,8 @@ zha_status zha_prefix_attn_decode(const zha_pages* p, const void* d_Q, zha_dtype
   PrefixArgs a;
   const bool tensor = tensor_path(p, q_dtype);
   if (!plan(p, batch, q_heads, nq, prefix_tokens, tensor, o_dtype == ZHA_F32, &a.s)) return ZHA_ERR_UNSUPPORTED;
-  if (scratch_bytes < zha_prefix_attn_scratch_bytes(p, batch, q_heads, nq, prefix_tokens)) return ZHA_ERR_INVALID_ARG;
-  const Scratch x = scratch_of(p, a.s);
+  const Scratch x = scratch_of(p, a.s);  // of the plan that will run
+  if (scratch_bytes < x.bytes) return ZHA_ERR_INVALID_ARG;
   char* base = static_cast<char*>(d_scratch);
   a.s.causal = causal != 0;
   a.s.prefix_seq = prefix_tokens > 0 ? prefix_seq : 0;
