@@ -407,9 +407,10 @@ zha_status zha_pages_gather(const zha_pages* pages, const void* d_K, const void*
  * kv_heads * rows > 2^30, or 2^31 tiles of work, counted for sequences of max_seq_pages pages: of 128 rows and
  * 128 keys (64 for an fp32 output) for bf16 queries over a bf16 cache, of 64 rows (16, where a sequence has no more) and 32
  * keys for other types.
- * bf16 queries over a bf16 cache run on the tensor cores: products are exact, sums fp32; for a bf16 output
- * the softmax weights are rounded to bf16 before they meet V, for an fp32 output they keep 24 bits.
- * All other types run in fp32. */
+ * bf16 queries over a bf16 cache run on the tensor cores: products are exact, sums fp32 and cut off instead of rounded (by
+ * 4.5e-5 of an output at most on average for a bf16 output, 1.8e-6 for an fp32 one, whatever the length); for a bf16 output
+ * the softmax weights are rounded to bf16 before they meet V (2^-8 of each; an eighth of them has an exp2 that is off
+ * by up to 1.1e-4 of itself before that), for an fp32 output they keep 24 bits.  All other types run in fp32. */
 size_t zha_prefix_attn_scratch_bytes(const zha_pages* pages, int batch, int q_heads, int nq, long long prefix_tokens);
 zha_status zha_prefix_attn_decode(const zha_pages* pages, const void* d_Q, zha_dtype q_dtype, int batch, int q_heads,
                                   int nq, const void* d_K, const void* d_V, const int* d_seqs, int prefix_seq,

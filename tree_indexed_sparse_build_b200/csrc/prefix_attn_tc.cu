@@ -43,8 +43,9 @@ __host__ __device__ constexpr int keys_of(bool wide) { return wide ? 64 : 128; }
 // memory.  The tensor core cuts its sums off instead of rounding them: at each of the 12 MMAs of a tile with an fp32 output
 // they lose 1.6e-8 of themselves on average.  Without end, an output over 120,000 tokens was off by 2.1e-5; with 16 tiles a
 // sum 3.5e-6, with 8 1.8e-6, with 4 1.0e-6, for 61, 61, 65 and 71 us of eight sequences of four queries on 32,768 tokens.
-// (A bf16 output's sums may lose 1e-4 on their way through a share of 1,000 tiles, a twentieth of its weights' rounding.)
-__host__ __device__ constexpr int tiles_per_sum(bool wide) { return wide ? 8 : 1 << 30; }
+// A bf16 output's tiles of 8 MMAs lose 1.4e-8 at each: sums of 8,192 tiles made outputs 9.4e-4 too small, those of 256
+// 4.5e-5, a fiftieth of what the rounding of the weights takes off or adds at random.
+__host__ __device__ constexpr int tiles_per_sum(bool wide) { return wide ? 8 : 256; }
 constexpr int kThreads = 384;
 constexpr int kTmemCols = 512;
 constexpr int kByFma = 2;     // of 16 pairs of weights, those whose exp2 the FMA pipes compute
@@ -238,7 +239,7 @@ struct Loader {
       const Segment g = x.g;
       const bool with_queries = KEYS && x.t == x.g.t0;
       int flags = dual ? kPaired : 0;
-      const bool sums = !KEYS && WIDE;  // first and last of a sum, else of the segment
+      const bool sums = !KEYS;  // first and last of a sum, else of the segment
       const int j = (x.t - x.g.t0) >> (by - 1);
       if (sums ? j % tiles_per_sum(WIDE) == 0 : j == 0) flags |= kFirst;
       if (x.t + by >= x.g.t1 || (sums && (j + 1) % tiles_per_sum(WIDE) == 0)) flags |= kLast;
@@ -546,6 +547,43 @@ struct Stream {
     __syncwarp();
   }
 
+  // Adds a bf16 output's sum, whose weights refer to m, to the one in memory, a row a thread.  Once in 256 tiles: short code
+  // rather than quick.  (As the stores and reductions of segment(), or as a function to call, it cost the segments that
+  // never come here more registers or instructions: 33 sequences of up to 4,000 tokens 63.5 and 65 us, this way 62.5,
+  // without any of it 61.7.)
+  __device__ __forceinline__ void add_sum(size_t slot, bool valid) {
+    __syncwarp();  // other lanes' stores
+    float by = 1.f, old = 1.f;  // what this sum is multiplied by, and the one in memory
+    if (valid) {
+      const float before = a.ml[slot + lane].x;
+      // (up to 2^16 this sum is scaled, which leaves it finite; more is rare, and what is there is scaled)
+      if (m <= before + 2 * kSlack)
+        by = m == before ? 1.f : exp2_approx(m - before);
+      else
+        old = before == -INFINITY ? 0.f : exp2_approx(before - m);
+      a.ml[slot + lane] = make_float2(old == 1.f ? before : m, l * by);
+    }
+    float* p = a.acc + (slot + lane) * D;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 16) {
+      __syncwarp();
+      uint32_t y[16];
+      tmem_ld16(y, to + c);
+      tmem_wait_ld();
+      if (!valid) continue;
+#pragma unroll
+      for (int k = 0; k < 16; k += 4) {
+        float4 x = __ldcg(reinterpret_cast<float4*>(p + c + k));
+        x.x = fmaf(x.x, old, __uint_as_float(y[k]) * by);
+        x.y = fmaf(x.y, old, __uint_as_float(y[k + 1]) * by);
+        x.z = fmaf(x.z, old, __uint_as_float(y[k + 2]) * by);
+        x.w = fmaf(x.w, old, __uint_as_float(y[k + 3]) * by);
+        __stcg(reinterpret_cast<float4*>(p + c + k), x);
+      }
+    }
+    __syncwarp();
+  }
+
   // This stream's tiles j0, j0 + by, .. of a segment that starts with the share's tile `tile0`.
   __device__ __forceinline__ bool segment(const Segment& g, int j0, int by, uint32_t tile0) {
     constexpr int kKeys = keys_of(WIDE), kQuarter = kKeys / 4;
@@ -587,7 +625,7 @@ struct Stream {
     float put_m = -INFINITY;  // WIDE: the maximum that the sums in memory refer to
     int j = j0;
     do {
-      const int sum0 = j, sum1 = WIDE ? min(n, j + tiles_per_sum(WIDE) * by) : n;  // the tiles of one sum
+      const int sum0 = j, sum1 = min(n, j + tiles_per_sum(WIDE) * by);  // the tiles of one sum
       for (; j < sum1; j += by) {
         const int k0 = first + (g.t0 + j) * kKeys, left = min(kKeys, g.len - k0);  // first key, keys
         if (!wait(&bars.s_full[st], ns++ & 1)) return false;
@@ -607,11 +645,11 @@ struct Stream {
         }
         if (work) {
           if (parts == 4) {
-            weigh<kQuarter>(kQuarter * quarter, row_end - k0 - kQuarter * quarter, j == sum0);
+            weigh<kQuarter>(kQuarter * quarter, row_end - k0 - kQuarter * quarter, j == (WIDE ? sum0 : j0));
             __syncwarp();
             clear_others();
           } else {
-            weigh<kKeys>(0, row_end - k0, j == sum0);
+            weigh<kKeys>(0, row_end - k0, j == (WIDE ? sum0 : j0));
           }
           tmem_wait_st();
         }
@@ -624,46 +662,50 @@ struct Stream {
       if (work) {
         const int part = g.kind == kDual ? st : (j0 * parts + (parts == 4 ? quarter : 0));
         const size_t slot = (size_t)g.slot + part * rows + (parts == 4 ? 0 : quarter * 32);  // of this warp's first row
-        float fix = 1.f;  // WIDE: from what this sum's weights refer to, to what the sums in memory do
-        if (WIDE) {
-          if (sum0 == j0) put_m = m;
-          // (up to 2^16 this sum is scaled, which leaves it finite; more is rare, and what is there is scaled)
-          if (__any_sync(0xffffffffu, m != put_m && !(m <= put_m + 2 * kSlack))) {
-            rescale(slot, valid, put_m == -INFINITY ? 0.f : exp2_approx(put_m - m));
-            put_m = m;
+        if (!WIDE && sum0 > j0) {
+          add_sum(slot, valid);
+        } else {
+          float fix = 1.f;  // WIDE: from what this sum's weights refer to, to what the sums in memory do
+          if (WIDE) {
+            if (sum0 == j0) put_m = m;
+            // (up to 2^16 this sum is scaled, which leaves it finite; more is rare, and what is there is scaled)
+            if (__any_sync(0xffffffffu, m != put_m && !(m <= put_m + 2 * kSlack))) {
+              rescale(slot, valid, put_m == -INFINITY ? 0.f : exp2_approx(put_m - m));
+              put_m = m;
+            }
+            if (m != put_m) fix = exp2_approx(m - put_m);
           }
-          if (m != put_m) fix = exp2_approx(m - put_m);
-        }
-        if (valid) a.ml[slot + lane] = WIDE ? make_float2(put_m, l * fix) : make_float2(m, l);
-        // in whole 32-byte sectors: a row a thread, 16 bytes at a time, took four times as long (13,000 clocks)
-        const unsigned some = __ballot_sync(0xffffffffu, valid);
+          if (valid) a.ml[slot + lane] = WIDE ? make_float2(put_m, l * fix) : make_float2(m, l);
+          // in whole 32-byte sectors: a row a thread, 16 bytes at a time, took four times as long (13,000 clocks)
+          const unsigned some = __ballot_sync(0xffffffffu, valid);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (!(some >> (16 * i) & 0xffffu)) continue;
-          const int r0 = 16 * i + lane / 4;
-          const float f0 = WIDE ? __shfl_sync(0xffffffffu, fix, r0) : 0.f, f1 = WIDE ? __shfl_sync(0xffffffffu, fix, r0 + 8) : 0.f;
-          float* out = a.acc + (slot + r0) * D + lane % 4 * 2;
+          for (int i = 0; i < 2; ++i) {
+            if (!(some >> (16 * i) & 0xffffu)) continue;
+            const int r0 = 16 * i + lane / 4;
+            const float f0 = WIDE ? __shfl_sync(0xffffffffu, fix, r0) : 0.f, f1 = WIDE ? __shfl_sync(0xffffffffu, fix, r0 + 8) : 0.f;
+            float* out = a.acc + (slot + r0) * D + lane % 4 * 2;
 #pragma unroll
-          for (int c = 0; c < D; c += 64) {
-            uint32_t y[32];
-            tmem_ld_blocks(y, to + (16u * i << 16) + c);
-            tmem_wait_ld();
-            if (WIDE && sum0 > j0) {
+            for (int c = 0; c < D; c += 64) {
+              uint32_t y[32];
+              tmem_ld_blocks(y, to + (16u * i << 16) + c);
+              tmem_wait_ld();
+              if (WIDE && sum0 > j0) {
 #pragma unroll
-              for (int k = 0; k < 16; ++k)
-                if (some >> (r0 + k % 2 * 8) & 1)
-                  add_to(out + k % 2 * 8 * D + c + k / 2 * 8, __uint_as_float(y[2 * k]) * (k & 1 ? f1 : f0),
-                         __uint_as_float(y[2 * k + 1]) * (k & 1 ? f1 : f0));
-              continue;
-            }
-            if (some >> r0 & 1) {
+                for (int k = 0; k < 16; ++k)
+                  if (some >> (r0 + k % 2 * 8) & 1)
+                    add_to(out + k % 2 * 8 * D + c + k / 2 * 8, __uint_as_float(y[2 * k]) * (k & 1 ? f1 : f0),
+                           __uint_as_float(y[2 * k + 1]) * (k & 1 ? f1 : f0));
+                continue;
+              }
+              if (some >> r0 & 1) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) *reinterpret_cast<uint2*>(out + c + 8 * k) = make_uint2(y[4 * k], y[4 * k + 1]);
-            }
-            if (some >> (r0 + 8) & 1) {
+                for (int k = 0; k < 8; ++k) *reinterpret_cast<uint2*>(out + c + 8 * k) = make_uint2(y[4 * k], y[4 * k + 1]);
+              }
+              if (some >> (r0 + 8) & 1) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<uint2*>(out + 8 * D + c + 8 * k) = make_uint2(y[4 * k + 2], y[4 * k + 3]);
+                for (int k = 0; k < 8; ++k)
+                  *reinterpret_cast<uint2*>(out + 8 * D + c + 8 * k) = make_uint2(y[4 * k + 2], y[4 * k + 3]);
+              }
             }
           }
         }
@@ -671,7 +713,7 @@ struct Stream {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.o_free[st]);
-    } while (WIDE && j < n);
+    } while (j < n);
     return true;
   }
 
