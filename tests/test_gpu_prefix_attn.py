@@ -548,3 +548,24 @@ def test_scratch_of_a_call_that_only_bf16_queries_fit():
     with pytest.raises(zha.ZhaError) as e:
         pages.attend(q.float(), k, v, 0.1, seqs)
     assert e.value.status == zha.ZHA_ERR_UNSUPPORTED
+
+
+def test_calls_ask_for_shared_memory_once():
+    # what a call asks of the CUDA runtime after the first of its kind: two launches, and nothing about its kernels
+    from torch.profiler import ProfilerActivity, profile
+    zha = _zha()
+    for kv, out in ((BF16, BF16), (BF16, F32), (F32, F32)):
+        for d in (64, 128):
+            pages, Q, K, V, table = _case(zha, 2, 2, d, 16, 32, [40, 50], 1, kv, kv)
+            q, k, v, s = Q.cuda(), K.cuda(), V.cuda(), _i32([0, 1])
+            pages.attend(q, k, v, 0.1, s, 0, 32, out_dtype=out)
+            torch.cuda.synchronize()
+            with profile(activities=[ProfilerActivity.CPU, ProfilerActivity.CUDA]) as prof:
+                pages.attend(q, k, v, 0.1, s, 0, 32, out_dtype=out)
+                torch.cuda.synchronize()
+            names = [e.name for e in prof.events()]
+            launches = sum(n.startswith(("cudaLaunchKernelExC", "cuLaunchKernelEx")) for n in names)
+            if launches == 0:
+                pytest.skip("the profiler sees no calls of the runtime")
+            assert launches == 2, names
+            assert not any("FuncSetAttribute" in n for n in names), names
