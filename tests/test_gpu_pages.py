@@ -310,3 +310,31 @@ def test_rows_far_behind_two_to_the_31():
     pages.gather(K, V, _i32([1]), out[:1], vout[:1])
     assert torch.equal(out[:1], rows)
     assert pages.check() == zha.ZHA_OK
+
+
+def test_launches_are_counted_from_several_threads():
+    # calls that only read a cache may overlap; sixteen threads gather from one
+    import threading
+    zha = _zha()
+    pages = zha.Pages(1, 64, 8, 4, 2, 2, torch.float32)
+    K, V = pages.pools()
+    pages.append(K, V, _i32([0]), torch.zeros((1, 1, 5, 64), device="cuda"), torch.zeros((1, 1, 5, 64), device="cuda"))
+    seqs = _i32([0])
+    out = [torch.empty((1, 1, 8, 64), device="cuda") for _ in "KV"]
+    before, each, threads = pages.launches, 1000, 16
+    call, args = zha.lib().zha_pages_gather, (K.data_ptr(), V.data_ptr(), seqs.data_ptr(), 1, out[0].data_ptr(),
+                                              out[1].data_ptr(), 8, torch.cuda.current_stream().cuda_stream)
+    start, bad = threading.Barrier(threads), []
+
+    def work():
+        with torch.cuda.device(0):
+            start.wait()
+            bad.extend(s for s in (call(pages.handle, *args) for _ in range(each)) if s)
+
+    all_threads = [threading.Thread(target=work) for _ in range(threads)]
+    for t in all_threads:
+        t.start()
+    for t in all_threads:
+        t.join()
+    assert not bad and pages.check() == zha.ZHA_OK
+    assert pages.launches == before + each * threads

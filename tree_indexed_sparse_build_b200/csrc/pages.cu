@@ -801,11 +801,11 @@ zha_status launch_rows(zha_pages* p, const RowArgs& x, long long bytes, unsigned
   cudaError_t e;
   if (bytes <= kSmallBytes) {
     e = launch_pdl(small_kernel<MODE>, dim3(1), dim3(kPlanThreads), 0, s, x);
-    p->launches += 1;
+    count_launches(p, 1);
   } else {
     e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, x.d, x.s, x.src, x.dst, x.counts, x.n, x.T, (int)MODE);
     if (e == cudaSuccess) e = launch_pdl(rows_kernel<MODE>, dim3(grid_x, x.n), dim3(kRowThreads), 0, s, x);
-    p->launches += 2;
+    count_launches(p, 2);
   }
   return cuda_status(e);
 }
@@ -889,7 +889,7 @@ zha_status zha_pages_load(zha_pages* p, const int* d_table, const int* d_lens, v
   cudaError_t e = launch_pdl(load_count_kernel, columns, block, 0, s, p->v, d_table, d_lens);
   if (e == cudaSuccess) e = launch_pdl(load_check_kernel, dim3(p->sms), block, 0, s, p->v);
   if (e == cudaSuccess) e = launch_pdl(load_apply_kernel, dim3(4 * p->sms), block, 0, s, p->v, d_table, d_lens);
-  p->launches += 3;
+  count_launches(p, 3);
   return cuda_status(e);
 }
 
@@ -945,13 +945,13 @@ zha_status zha_pages_free(zha_pages* p, const int* d_seqs, int n, void* stream) 
   if (st != ZHA_OK || skip) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if ((long long)n * p->desc.max_seq_pages <= kFewPages) {
-    p->launches += 1;
+    count_launches(p, 1);
     return cuda_status(launch_pdl(free_kernel, dim3(n), dim3(kRowThreads), 0, s, p->v, d_seqs));
   }
   cudaError_t e = launch_pdl(free_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p->v, d_seqs, n);
   if (e == cudaSuccess)
     e = launch_pdl(free_columns_kernel, dim3(column_grid(p), (n + kRun - 1) / kRun), dim3(kRowThreads), 0, s, p->v, d_seqs, n);
-  p->launches += 2;
+  count_launches(p, 2);
   return cuda_status(e);
 }
 
@@ -961,7 +961,7 @@ zha_status zha_pages_compact(zha_pages* p, void* d_K, void* d_V, int* d_live, vo
   cudaError_t e = launch_pdl(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p->v, d_live);
   if (e == cudaSuccess)
     e = launch_pdl(compact_move_kernel, dim3(8 * p->sms), dim3(kRowThreads), 0, s, p->v, (uint4*)d_K, (uint4*)d_V);
-  p->launches += 2;
+  count_launches(p, 2);
   return cuda_status(e);
 }
 
@@ -976,7 +976,7 @@ zha_status zha_pages_gather(const zha_pages* p, const void* d_K, const void* d_V
   const cudaError_t e = launch_pdl(gather_kernel, grid, dim3(kRowThreads), 0, static_cast<cudaStream_t>(stream), p->v,
                                    d_seqs, capacity_tokens, (const uint4*)d_K, (const uint4*)d_V, (uint4*)d_Kout,
                                    (uint4*)d_Vout);
-  const_cast<zha_pages*>(p)->launches += 1;  // the handle is logically const
+  count_launches(p, 1);
   return cuda_status(e);
 }
 
@@ -999,7 +999,7 @@ zha_status zha_pages_check(zha_pages* p, void* stream) {
 const int* zha_pages_table(const zha_pages* p) { return p ? p->v.table : nullptr; }
 const int* zha_pages_lens(const zha_pages* p) { return p ? p->v.lens : nullptr; }
 const int* zha_pages_refs(const zha_pages* p) { return p ? p->v.refs : nullptr; }
-long long zha_pages_launch_count(const zha_pages* p) { return p ? p->launches : -1; }
+long long zha_pages_launch_count(const zha_pages* p) { return p ? __atomic_load_n(&p->launches, __ATOMIC_RELAXED) : -1; }
 int zha_pages_device(const zha_pages* p) { return p ? p->device : -1; }
 
 zha_status zha_pages_get_desc(const zha_pages* p, zha_pages_desc* out) {

@@ -44,11 +44,15 @@ struct zha_pages {
   zha::PagesView v;
   int sms;
   int device;
-  long long launches;
+  long long launches;  // (changed by count_launches alone: calls that only read the cache may overlap)
   long long wait_limit;
 };
 
 namespace zha {
+
+inline void count_launches(const zha_pages* p, int n) {
+  __atomic_fetch_add(&const_cast<zha_pages*>(p)->launches, n, __ATOMIC_RELAXED);  // the handle is logically const
+}
 
 // True when the pages' device is the current one (launches go to the current device).
 inline bool on_device(const zha_pages* p) {

@@ -561,7 +561,7 @@ zha_status zha_prefix_attn_decode(const zha_pages* p, const void* d_Q, zha_dtype
                   : d == 64 ? launch_fp32_types<64>(p, a, q_dtype, p->desc.kv_dtype, s)
                             : launch_fp32_types<128>(p, a, q_dtype, p->desc.kv_dtype, s);
   if (e == cudaSuccess) e = d == 64 ? launch_join<64>(a, o_dtype, s) : launch_join<128>(a, o_dtype, s);
-  const_cast<zha_pages*>(p)->launches += 2;  // the handle is logically const
+  count_launches(p, 2);
   return e == cudaSuccess ? ZHA_OK : ZHA_ERR_CUDA;
 }
 
