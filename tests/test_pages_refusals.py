@@ -177,3 +177,19 @@ def test_scratch_of_a_call_that_only_some_types_fit(geometry, q_heads, nq, batch
     # a row's maximum, sum and head_dim values, for every row at least
     assert many >= batches[1] * q_heads * nq * (geometry["head_dim"] + 2) * 4 and few >= many * batches[0] // batches[1] // 2
     assert size(h, 2 ** 20 + 1, q_heads, nq, 0) == 0 and size(h, 1, q_heads, 2 ** 20 + 1, 0) == 0
+
+
+def test_calls_with_another_device_current():
+    # .. than the handle's, or none at all: refused before anything is launched, copied or read
+    lib, p, h, g = zha.lib(), ctypes.c_void_p(0x1000), _handle(), _handle()
+    bad = zha.ZHA_ERR_INVALID_ARG
+    assert lib.zha_pages_load(h, p, p, None) == bad
+    assert lib.zha_pages_append(h, p, p, p, 1, p, p, 1, None, None) == bad
+    assert lib.zha_pages_fork(h, p, p, p, p, 1, None) == bad
+    assert lib.zha_pages_copy(g, p, p, h, p, p, p, p, 1, None) == bad
+    assert lib.zha_pages_free(h, p, 1, None) == bad
+    assert lib.zha_pages_compact(h, p, p, None, None) == bad
+    assert lib.zha_pages_gather(h, p, p, p, 1, p, p, 8, None) == bad
+    assert lib.zha_prefix_attn_decode(h, p, 1, 1, 2, 1, p, p, p, 0, 0, 0, F(1.0), p, 1, p, 1 << 20, None) == bad
+    # (the default stream is the current device's: a check on it would not wait for the cache's work)
+    assert lib.zha_pages_check(h, None) == bad

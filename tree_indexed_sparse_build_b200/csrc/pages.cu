@@ -981,7 +981,7 @@ zha_status zha_pages_gather(const zha_pages* p, const void* d_K, const void* d_V
 }
 
 zha_status zha_pages_check(zha_pages* p, void* stream) {
-  if (!p) return ZHA_ERR_INVALID_ARG;
+  if (!p || !on_device(p)) return ZHA_ERR_INVALID_ARG;  // (stream 0 is the current device's)
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   unsigned h = 0;
   if (cudaMemcpyAsync(&h, p->v.err, sizeof(h), cudaMemcpyDeviceToHost, s) != cudaSuccess ||

@@ -651,7 +651,8 @@ def zha_pages_gather(handle, K: torch.Tensor, V: torch.Tensor, seqs: torch.Tenso
 
 
 def zha_pages_check(handle, stream=None) -> int:
-    return int(lib().zha_pages_check(handle, _raw_stream(handle, stream)))
+    with torch.cuda.device(zha_pages_device(handle)):
+        return int(lib().zha_pages_check(handle, _raw_stream(handle, stream)))
 
 
 def zha_prefix_attn_scratch_bytes(handle, batch: int, q_heads: int, nq: int, prefix_tokens: int) -> int:
