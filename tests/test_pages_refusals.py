@@ -193,3 +193,20 @@ def test_calls_with_another_device_current():
     assert lib.zha_prefix_attn_decode(h, p, 1, 1, 2, 1, p, p, p, 0, 0, 0, F(1.0), p, 1, p, 1 << 20, None) == bad
     # (the default stream is the current device's: a check on it would not wait for the cache's work)
     assert lib.zha_pages_check(h, None) == bad
+
+
+def test_pools_that_a_copy_reads(monkeypatch):
+    # the pools that are named are the ones that are read, and another cache's have to be named
+    calls = []
+    monkeypatch.setattr(zha, "zha_pages_copy", lambda *a: calls.append(a))
+    pages, other = (object.__new__(zha.Pages) for _ in range(2))
+    pages.handle, other.handle = None, None
+    K, V, A, B, s = (object() for _ in range(5))
+    pages.copy(K, V, s, s)
+    pages.copy(K, V, s, s, K_from=A, V_from=B)
+    pages.copy(K, V, s, s, source=other, K_from=A, V_from=B)
+    assert [c[1:3] for c in calls] == [(K, V), (A, B), (A, B)]
+    for kw in (dict(source=other), dict(source=other, K_from=A), dict(K_from=A), dict(V_from=B)):
+        with pytest.raises(ValueError, match="K_from and V_from"):
+            pages.copy(K, V, s, s, **kw)
+    assert len(calls) == 3

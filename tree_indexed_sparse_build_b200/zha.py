@@ -933,9 +933,14 @@ class Pages:
 
     def copy(self, K: torch.Tensor, V: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, stream=None,
              source: "Pages | None" = None, K_from: torch.Tensor | None = None, V_from: torch.Tensor | None = None):
-        """Copy sequences src of `source` (pools K_from, V_from; default: this cache) to empty slots dst."""
+        """Copy sequences src of `source` (default: this cache) from pools K_from, V_from (default: K, V) to
+        empty slots dst."""
+        if (K_from is None) != (V_from is None) or (source is not None and K_from is None):
+            raise ValueError("K_from and V_from go together, and a source cache needs both")
         if source is None:
-            source, K_from, V_from = self, K, V
+            source = self
+        if K_from is None:
+            K_from, V_from = K, V
         zha_pages_copy(source.handle, K_from, V_from, self.handle, K, V, src, dst, stream)
 
     def free(self, seqs: torch.Tensor, stream=None):
