@@ -14,7 +14,7 @@ BF16, F32 = torch.bfloat16, torch.float32
 
 @pytest.fixture(scope="module", autouse=True)
 def _give_memory_back():
-    yield  # the largest pools here hold half a GB
+    yield  # the largest pools here hold a GB and more
     if torch.cuda.is_available():
         torch.cuda.empty_cache()
 
@@ -200,3 +200,24 @@ def test_weights_for_an_fp32_output_keep_24_bits():
     high = w.float().to(BF16)
     two = high.double() + (w.float() - high.float()).to(BF16).double()
     assert ((two / w - 1).abs() > limit).any()
+
+
+@pytest.mark.parametrize("shared,batch,group", [(True, 4, 2), (True, 16, 4), (False, 1, 4), (False, 1, 48)])
+def test_long_sums_of_few_rows(shared, batch, group):
+    # 276 tiles a stream and CTA, so that its sum ends once on the way, of rows that fill a warp, a tile in part, or
+    # more than a warp of one sequence's own tokens.  A sum that is lost or counted twice is a fortieth of
+    # the keys, 16% of a row's norm; the bound is 4 2^-8 as above.
+    zha = _zha()
+    heads, d, page, n = 8, 64, 256, 1310720
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    K, V = (torch.randn((n // page, heads, page, d), generator=gen, device="cuda", dtype=BF16) for _ in "KV")
+    Q = torch.randn((batch, heads * group, 1, d), generator=gen, device="cuda").to(BF16)
+    pages = _shared(zha, heads, d, page, n, batch)
+    got = pages.attend(Q, K, V, d ** -0.5, _i32(list(range(batch))), 0, n if shared else 0)
+    assert pages.check() == zha.ZHA_OK
+    for h in range(heads):
+        q, x = (t[:, h * group:(h + 1) * group].reshape(-1, d).double() for t in (Q, got))
+        k, v = (t[:, h].reshape(-1, d).double() for t in (K, V))
+        for i in range(0, len(q), 16):
+            o = torch.softmax(q[i:i + 16] @ k.T * d ** -0.5, -1) @ v
+            assert ((x[i:i + 16] - o).norm(dim=-1) <= 4 * 2.0 ** -8 * o.norm(dim=-1)).all(), (h, i)
