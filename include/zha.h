@@ -326,7 +326,7 @@ zha_status zha_tree_set_wait_limit(zha_tree* tree, long long cycles);
  * (gather, attention) may overlap one another.
  * (The source pages have no counterpart: the cache of their method is dense.) */
 typedef struct {
-  int kv_heads;      /* >= 1                                                          */
+  int kv_heads;      /* 1 .. 65535                                                    */
   int head_dim;      /* 64 or 128                                                     */
   int page_tokens;   /* a power of two, 8 .. 256                                      */
   int num_pages;     /* >= 1; num_pages * kv_heads <= 2^30                            */
@@ -353,7 +353,8 @@ zha_status zha_pages_destroy(zha_pages* pages); /* the handle only; the workspac
 zha_status zha_pages_load(zha_pages* pages, const int* d_table, const int* d_lens, void* stream);
 
 /* Appends tokens to the listed sequences: d_Knew, d_Vnew [n, kv_heads, tokens, head_dim] in
- * kv_dtype; entry i appends its first d_counts[i] (0 .. tokens; NULL: all). */
+ * kv_dtype; entry i appends its first d_counts[i] (0 .. tokens; NULL: all).  tokens * kv_heads <= 2^30
+ * (ZHA_ERR_UNSUPPORTED). */
 zha_status zha_pages_append(zha_pages* pages, void* d_K, void* d_V, const int* d_seqs, int n, const void* d_Knew,
                             const void* d_Vnew, int tokens, const int* d_counts, void* stream);
 
@@ -401,14 +402,15 @@ zha_status zha_pages_gather(const zha_pages* pages, const void* d_K, const void*
  *                  overlap need one each
  * Rows of the pools that hold no token are never used, whatever they contain.  A slot out of range
  * counts as an empty sequence, a page id out of range as a page of zeros; those, and a prefix longer than
- * prefix_seq, set ZHA_ERR_DEVICE.  Values of tokens that any query of a call sees must be finite.
+ * prefix_seq, set ZHA_ERR_DEVICE.  Values of tokens that any query of a call sees, and of the
+ * prefix's tokens, must be finite.
  * A score that is NaN or +infinity makes its query's output NaN and no other's.
  * ZHA_ERR_UNSUPPORTED where an index would not fit: rows = q_heads / kv_heads * nq > 2^20, batch > 2^20, batch *
- * kv_heads * rows > 2^30, or 2^31 tiles of work, counted for sequences of max_seq_pages pages: of 128 rows and
- * 128 keys (64 for an fp32 output) for bf16 queries over a bf16 cache, of 64 rows (16, where a sequence has no more) and 32
- * keys for other types.
- * bf16 queries over a bf16 cache run on the tensor cores: products are exact, sums fp32 and cut off instead of rounded (by
- * 4.5e-5 of an output at most on average for a bf16 output, 1.8e-6 for an fp32 one, whatever the length); for a bf16 output
+ * kv_heads * rows > 2^30, or 2^31 units of work, counted for sequences of max_seq_pages pages.  A unit is a tile of 128 rows
+ * and 128 keys (64 for an fp32 output) for bf16 queries over a bf16 cache, of 64 rows (16, where a sequence has no more) and
+ * 32 keys for other types; a tile of the prefix is up to five.
+ * bf16 queries over a bf16 cache run on the tensor cores: products are exact, sums fp32 and cut off instead of rounded
+ * (outputs are too small by about 4.5e-5 of themselves in bf16 and 1.8e-6 in fp32, however long the sums); for a bf16 output
  * the softmax weights are rounded to bf16 before they meet V (2^-8 of each; an eighth of them has an exp2 that is off
  * by up to 1.1e-4 of itself before that), for an fp32 output they keep 24 bits.  All other types run in fp32. */
 size_t zha_prefix_attn_scratch_bytes(const zha_pages* pages, int batch, int q_heads, int nq, long long prefix_tokens);

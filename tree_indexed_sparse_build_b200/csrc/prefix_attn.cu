@@ -19,8 +19,9 @@ constexpr int kKeys = 32;  // keys per tile of the fp32 kernel
 // running maximum and sum (the 16 threads of a row agree on them by shuffles) and
 // accumulates columns 4 tx .. of the same rows.  The next tile's keys and values are on their way in registers,
 // and the page ids of the one after, while a tile is computed; two CTAs share an SM.  (64 keys a tile and one
-// buffer for K and V in turn, loads exposed: 16 sequences of 1,400 tokens 27 us.)  Bound: latency of the few tiles a CTA
-// has.  16 sequences of 700 own tokens on 1,008 shared, 8 query and 2 KV heads of 128: 24 us with the join, which takes 9.
+// buffer for K and V in turn, loads exposed: 16 sequences of 1,400 tokens 27 us.)  Bound: latency: a small call's CTAs have a
+// tile or two each, and finding them (dependent loads and sums over the batch) takes as long.  16 sequences of up to 700 own
+// tokens on 1,008 shared, 8 query and 2 KV heads of 128: 24 us with the join, which takes 9.
 template <int D, typename TQ, typename TKV>
 struct Fp32Tile {
   static constexpr int kStride = D + 4;  // 16 rows apart by 4 banks: float4 reads without conflicts
@@ -255,8 +256,11 @@ __global__ void __launch_bounds__(kThreads, 2) fp32_kernel(const __grid_constant
 //
 // One CTA for up to four rows of a sequence and head: its warps take the rows' partial results in turn (finding one
 // takes longer than reading it, and it is found for all the rows at once), rescale by the maxima and
-// add (fp32); the order is fixed, so the result does not depend on timing.  Bound: latency of a row's parts (at most 30 or
-// so) after the division that finds them.  2,048 rows of 128 on a 131,072-token prefix: 14 of 207 us.
+// add (fp32); the order is fixed, so the result does not depend on timing.  Bound: latency of a row's parts, which the
+// warps read two at a time each, after the division that finds them.  An item leaves one part for each CTA that it is cut
+// over, times streams and quarters (8) for up to 32 rows on the tensor cores: 30 or so where there are many items, but 148 x 8
+// for one.  2,048 rows of 128 on a 131,072-token prefix: 14 of 200 us; one sequence of 131,072 tokens on one KV head (4 rows,
+// one CTA here): 85 us in all, where its keys and values take 10.
 constexpr int kJoinWarps = 8, kJoinRows = 4, kAtOnce = 2;
 
 template <int D>

@@ -77,8 +77,9 @@ __device__ __forceinline__ int tokens_seen(const PrefixShape& s, int len, int i)
   return s.causal ? len - s.nq + 1 + i : len;
 }
 
-// Costs, by what the tensor kernel takes: a dual tile about 3,900 clocks, any other (its 64 KB of keys
-// and values are the bound) 2,000 to 2,600, and so does the start and end of an own item.
+// Costs, by what the tensor kernel takes for a bf16 output: a dual tile about 3,900 clocks, any other (its 64 KB of keys
+// and values are the bound) 2,000 to 2,600, and so does the start and end of an own item.  (Tiles of 64 keys with three
+// products, for an fp32 output, are weighted alike; a run of lone ones takes about 3,000 clocks each.)
 constexpr int kDualCost = 2, kTileCost = 1, kOwnStart = 1;
 
 // Where CTA c's share of the cost T starts (c == ctas: T).
